@@ -5,7 +5,11 @@
 
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+#include <cmath>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <utility>
 
 #include "common.cuh"
@@ -18,6 +22,9 @@
 #include "scan.cuh"
 #include "bwd.cuh"
 #include "bwd_tc.cuh"
+#include "embed.cuh"
+#include "scan_bwd.cuh"
+#include "adamw.cuh"
 
 namespace {
 
@@ -528,6 +535,208 @@ mmf_status fwd_impl(const uint16_t* x, const float* gamma, float eps, int64_t M,
     return MMF_OK;
 }
 
+// ---------------------------------------------------------------------------
+// embedding
+// ---------------------------------------------------------------------------
+mmf_status check_embed_shape(int64_t V, int64_t M, int64_t K) {
+    if (V < 0 || M < 0 || K < 0) return MMF_ERR_INVALID_ARG;
+    if (K < 8 || (K % 8) != 0 || K > kMaxK || V >= kMaxDim || M > kMaxTokens) return MMF_ERR_UNSUPPORTED_SHAPE;
+    if (V * K > (int64_t(1) << 40)) return MMF_ERR_UNSUPPORTED_SHAPE;
+    return MMF_OK;
+}
+
+// How the embedding gradient splits M places: over the sorting CTAs (a
+// multiple of kSortThreads each) and over the summing CTAs.
+struct EmbedPlan {
+    int sort_per, sort_ctas;
+    int sum_per, sum_ctas;
+    int passes, digit_bits;
+};
+
+EmbedPlan embed_plan(int64_t V, int64_t M) {
+    EmbedPlan pl{};
+    if (M == 0) return pl;
+    const int64_t per = (M + kSortCtas - 1) / kSortCtas;
+    pl.sort_per = static_cast<int>((per + kSortThreads - 1) / kSortThreads * kSortThreads);
+    pl.sort_ctas = static_cast<int>((M + pl.sort_per - 1) / pl.sort_per);
+    pl.sum_per = M <= 131072 ? 64 : 256;
+    pl.sum_ctas = static_cast<int>((M + pl.sum_per - 1) / pl.sum_per);
+    int bits = 0;  // of the keys 0 .. V
+    while ((V >> bits) != 0) ++bits;
+    pl.passes = std::max(1, (bits + 7) / 8);
+    pl.digit_bits = (bits + pl.passes - 1) / pl.passes;
+    return pl;
+}
+
+struct EmbedWorkspace {
+    uint32_t* key[2];
+    uint32_t* pos[2];
+    int* count;
+    float* head;
+    float* tail;
+    size_t bytes;
+};
+
+EmbedWorkspace carve_embed(void* ws, const EmbedPlan& pl, int64_t M, int64_t K) {
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    size_t at = 0;
+    const auto take = [&](size_t bytes) {
+        uint8_t* r = b + at;
+        at += align256(bytes);
+        return r;
+    };
+    EmbedWorkspace w;
+    for (int i = 0; i < 2; ++i) {
+        w.key[i] = reinterpret_cast<uint32_t*>(take(4 * static_cast<size_t>(M)));
+        w.pos[i] = reinterpret_cast<uint32_t*>(take(4 * static_cast<size_t>(M)));
+    }
+    w.count = reinterpret_cast<int*>(take(sizeof(int) * kSortCtas * kSortBins));
+    const size_t parts = 4 * static_cast<size_t>(pl.sum_ctas) * static_cast<size_t>(K);
+    w.head = reinterpret_cast<float*>(take(parts));
+    w.tail = reinterpret_cast<float*>(take(parts));
+    w.bytes = at;
+    return w;
+}
+
+template <typename Id>
+mmf_status embed_sort(const void* ids, int64_t V, int64_t M, const EmbedPlan& pl, const EmbedWorkspace& w,
+                      cudaStream_t s) {
+    for (int i = 0; i < pl.passes; ++i) {
+        SortParams p{};
+        p.ids = ids;
+        p.key_in = w.key[(i + 1) & 1];
+        p.pos_in = w.pos[(i + 1) & 1];
+        p.key_out = w.key[i & 1];
+        p.pos_out = w.pos[i & 1];
+        p.count = w.count;
+        p.V = V;
+        p.M = static_cast<int>(M);
+        p.per = pl.sort_per;
+        p.shift = i * pl.digit_bits;
+        p.mask = (1 << pl.digit_bits) - 1;
+        const dim3 grid(static_cast<unsigned>(pl.sort_ctas)), block(kSortThreads);
+        mmf_status st = i == 0 ? launch(embed_count_kernel<Id, true>, grid, block, 0, s, false, p)
+                               : launch(embed_count_kernel<Id, false>, grid, block, 0, s, false, p);
+        if (st != MMF_OK) return st;
+        st = i == 0 ? launch(embed_place_kernel<Id, true>, grid, block, 0, s, false, p)
+                    : launch(embed_place_kernel<Id, false>, grid, block, 0, s, false, p);
+        if (st != MMF_OK) return st;
+    }
+    return MMF_OK;
+}
+
+mmf_status check_scan_shape(int64_t B, int64_t T, int64_t D) {
+    if (B < 0 || T < 0 || D < 0) return MMF_ERR_INVALID_ARG;
+    if ((D % 2) != 0 || D > kMaxDim || T > kMaxDim || B > 65535) return MMF_ERR_UNSUPPORTED_SHAPE;
+    if (D > 0 && B * T > (int64_t(1) << 40) / D) return MMF_ERR_UNSUPPORTED_SHAPE;
+    return MMF_OK;
+}
+
+// ---------------------------------------------------------------------------
+// AdamW
+// ---------------------------------------------------------------------------
+constexpr int kAdamCap = 256;  // tensors per launch
+
+mmf_status adam_scalars(const mmf_adamw_hyper* h, mmf_adamw_scalars* out) {
+    const auto in01 = [](double b) { return b >= 0.0 && b < 1.0; };
+    if (!h || !out) return MMF_ERR_INVALID_ARG;
+    if (!in01(h->beta1) || !in01(h->beta2) || !(h->lr >= 0.0) || !(h->eps > 0.0) || h->step < 1 ||
+        !std::isfinite(static_cast<float>(h->lr)) || !std::isfinite(static_cast<float>(h->eps)) ||
+        !std::isfinite(static_cast<float>(h->grad_scale)))
+        return MMF_ERR_INVALID_ARG;
+    // what the kernel uses is fp32: an eps or a beta that rounds out of its range is refused too
+    if (!(static_cast<float>(h->eps) > 0.0f) || static_cast<float>(h->beta1) >= 1.0f ||
+        static_cast<float>(h->beta2) >= 1.0f)
+        return MMF_ERR_INVALID_ARG;
+    const double t = static_cast<double>(h->step);
+    out->lr = static_cast<float>(h->lr);
+    out->alpha = static_cast<float>(h->lr / (1.0 - std::pow(h->beta1, t)));
+    out->inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(h->beta2, t)));
+    out->grad_scale = static_cast<float>(h->grad_scale);
+    out->seed = h->seed;
+    out->reserved = 0;
+    return std::isfinite(out->alpha) ? MMF_OK : MMF_ERR_INVALID_ARG;
+}
+
+mmf_status adam_check_tensor(const mmf_adamw_tensor& t) {
+    if ((t.flags & ~(MMF_ADAMW_STATE8 | MMF_ADAMW_GRAD_BF16)) != 0 || t.n < 0) return MMF_ERR_INVALID_ARG;
+    if (!(t.weight_decay >= 0.0f) || !std::isfinite(t.weight_decay)) return MMF_ERR_INVALID_ARG;
+    if (t.n > (int64_t(1) << 40)) return MMF_ERR_UNSUPPORTED_SHAPE;
+    if (t.n == 0) return MMF_OK;
+    const bool eight = (t.flags & MMF_ADAMW_STATE8) != 0;
+    if (!t.p || !t.g || !t.m || !t.v || (eight && (!t.m_scale || !t.v_scale))) return MMF_ERR_INVALID_ARG;
+    if (!eight && (t.m_scale || t.v_scale)) return MMF_ERR_INVALID_ARG;
+    if (!aligned16(t.p) || !aligned16(t.g) || !aligned16(t.m) || !aligned16(t.v) || !aligned16(t.m_scale) ||
+        !aligned16(t.v_scale) || !aligned16(t.p_bf16))
+        return MMF_ERR_MISALIGNED;
+    return MMF_OK;
+}
+
+// Whether two of the buffers that a step writes overlap, or one that it writes
+// and a gradient that it reads.
+mmf_status adam_check_overlap(const mmf_adamw_tensor* tensors, int count) {
+    struct Range {
+        uintptr_t begin, end;
+        bool written;
+    };
+    std::unique_ptr<Range[]> r(new (std::nothrow) Range[static_cast<size_t>(count) * 7]);
+    if (!r) return MMF_ERR_INVALID_ARG;
+    size_t n = 0;
+    const auto add = [&](const void* p, int64_t bytes, bool written) {
+        const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+        if (p) r[n++] = {b, b + static_cast<uintptr_t>(bytes), written};
+    };
+    for (int i = 0; i < count; ++i) {
+        const mmf_adamw_tensor& t = tensors[i];
+        if (t.n == 0) continue;
+        const bool eight = (t.flags & MMF_ADAMW_STATE8) != 0;
+        const int64_t blocks = (t.n + kAdamBlock - 1) / kAdamBlock;
+        add(t.p, 4 * t.n, true);
+        add(t.g, t.n * ((t.flags & MMF_ADAMW_GRAD_BF16) ? 2 : 4), false);
+        add(t.m, t.n * (eight ? 1 : 4), true);
+        add(t.v, t.n * (eight ? 1 : 4), true);
+        add(t.m_scale, 4 * blocks, true);
+        add(t.v_scale, 4 * blocks, true);
+        add(t.p_bf16, 2 * t.n, true);
+    }
+    std::sort(r.get(), r.get() + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+    uintptr_t written_end = 0, read_end = 0;
+    for (size_t i = 0; i < n; ++i) {
+        if (r[i].begin < written_end || (r[i].written && r[i].begin < read_end)) return MMF_ERR_INVALID_ARG;
+        uintptr_t& end = r[i].written ? written_end : read_end;
+        end = std::max(end, r[i].end);
+    }
+    return MMF_OK;
+}
+
+template <int CAP>
+mmf_status launch_adamw(const mmf_adamw_tensor* tensors, int first, int count, const mmf_adamw_hyper* h,
+                        const mmf_adamw_scalars& sc, const mmf_adamw_scalars* scalars, cudaStream_t s) {
+    AdamParams<CAP> p;
+    int64_t chunks = 0;
+    for (int i = 0; i < count; ++i) {
+        const mmf_adamw_tensor& t = tensors[first + i];
+        p.t[i] = {t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.p_bf16, t.n,
+                  adam_key(sc.seed, static_cast<unsigned long long>(first + i)), t.weight_decay,
+                  ((t.flags & MMF_ADAMW_STATE8) ? kAdam8 : 0) | ((t.flags & MMF_ADAMW_GRAD_BF16) ? kAdamGradBf16 : 0)};
+        p.chunk_start[i] = static_cast<unsigned>(chunks);
+        chunks += (t.n + kAdamChunk - 1) / kAdamChunk;
+        if (chunks > kMaxDim) return MMF_ERR_UNSUPPORTED_SHAPE;
+    }
+    if (chunks == 0) return MMF_OK;
+    p.chunk_start[count] = static_cast<unsigned>(chunks);
+    p.count = count;
+    p.beta1 = static_cast<float>(h->beta1);
+    p.omb1 = static_cast<float>(1.0 - h->beta1);
+    p.beta2 = static_cast<float>(h->beta2);
+    p.omb2 = static_cast<float>(1.0 - h->beta2);
+    p.eps = static_cast<float>(h->eps);
+    p.host = {sc.lr, sc.alpha, sc.inv_sqrt_bc2, sc.grad_scale};
+    p.device = reinterpret_cast<const AdamScalars*>(scalars);
+    p.first = first;
+    return launch(adamw_kernel<CAP>, dim3(static_cast<unsigned>(chunks)), dim3(kAdamThreads), 0, s, false, p);
+}
+
 }  // namespace
 
 extern "C" {
@@ -845,6 +1054,126 @@ int mmf_mlgru_scan(const uint16_t* f_pre, const uint16_t* c_pre, const uint16_t*
     }
     return launch(mlgru_scan_kernel, grid, dim3(kScanWarps * 32), 0, static_cast<cudaStream_t>(stream), false, f_pre,
                   c_pre, g_pre, h0, static_cast<int>(T), static_cast<int>(D), o, h_last);
+}
+
+int mmf_embed_fwd(const void* ids, const void* table, float scale, int64_t V, int64_t M, int64_t K, uint16_t* x,
+                  unsigned flags, void* stream) {
+    if (!std::isfinite(scale) || (flags & ~(MMF_EMBED_IDS64 | MMF_EMBED_TABLE_BF16)) != 0) return MMF_ERR_INVALID_ARG;
+    mmf_status st = check_embed_shape(V, M, K);
+    if (st != MMF_OK) return st;
+    if (M == 0) return MMF_OK;
+    if (!ids || !x || (V > 0 && !table)) return MMF_ERR_INVALID_ARG;
+    if (!aligned16(ids) || !aligned16(table) || !aligned16(x)) return MMF_ERR_MISALIGNED;
+    DeviceState* dev;
+    if ((st = device_state(&dev)) != MMF_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const dim3 grid(static_cast<unsigned>(std::min(M, int64_t(dev->num_sms) * 8))), block(kEmbedThreads);
+    const bool wide = (flags & MMF_EMBED_IDS64) != 0, bf16 = (flags & MMF_EMBED_TABLE_BF16) != 0;
+    const int k = static_cast<int>(K);
+    const int32_t* i32 = static_cast<const int32_t*>(ids);
+    const int64_t* i64 = static_cast<const int64_t*>(ids);
+    if (wide)
+        return bf16 ? launch(embed_fwd_kernel<int64_t, true>, grid, block, 0, s, false, i64, table, V, M, k, scale, x)
+                    : launch(embed_fwd_kernel<int64_t, false>, grid, block, 0, s, false, i64, table, V, M, k, scale, x);
+    return bf16 ? launch(embed_fwd_kernel<int32_t, true>, grid, block, 0, s, false, i32, table, V, M, k, scale, x)
+                : launch(embed_fwd_kernel<int32_t, false>, grid, block, 0, s, false, i32, table, V, M, k, scale, x);
+}
+
+size_t mmf_embed_bwd_workspace_bytes(int64_t V, int64_t M, int64_t K) {
+    if (check_embed_shape(V, M, K) != MMF_OK || V == 0 || M == 0) return 0;
+    return carve_embed(nullptr, embed_plan(V, M), M, K).bytes;
+}
+
+int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, int64_t M, int64_t K, float* dtable,
+                  void* workspace, size_t workspace_bytes, unsigned flags, void* stream) {
+    if (!std::isfinite(scale) || (flags & ~(MMF_EMBED_IDS64 | MMF_EMBED_ACCUMULATE)) != 0) return MMF_ERR_INVALID_ARG;
+    mmf_status st = check_embed_shape(V, M, K);
+    if (st != MMF_OK) return st;
+    const bool accumulate = (flags & MMF_EMBED_ACCUMULATE) != 0;
+    if (V == 0 || (M == 0 && accumulate)) return MMF_OK;
+    if (!dtable || (M > 0 && (!ids || !dx))) return MMF_ERR_INVALID_ARG;
+    if (!aligned16(ids) || !aligned16(dx) || !aligned16(dtable) || !aligned16(workspace)) return MMF_ERR_MISALIGNED;
+    const EmbedPlan pl = embed_plan(V, M);
+    const EmbedWorkspace w = carve_embed(workspace, pl, M, K);
+    if (M > 0 && (!workspace || workspace_bytes < w.bytes)) return MMF_ERR_WORKSPACE;
+    DeviceState* dev;
+    if ((st = device_state(&dev)) != MMF_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!accumulate && cudaMemsetAsync(dtable, 0, 4 * static_cast<size_t>(V) * static_cast<size_t>(K), s) != cudaSuccess)
+        return MMF_ERR_CUDA;
+    if (M == 0) return MMF_OK;
+    st = (flags & MMF_EMBED_IDS64) ? embed_sort<int64_t>(ids, V, M, pl, w, s) : embed_sort<int32_t>(ids, V, M, pl, w, s);
+    if (st != MMF_OK) return st;
+    SumParams p{};
+    p.key = w.key[(pl.passes - 1) & 1];
+    p.pos = w.pos[(pl.passes - 1) & 1];
+    p.dx = dx;
+    p.dtable = dtable;
+    p.head = w.head;
+    p.tail = w.tail;
+    p.V = V;
+    p.M = static_cast<int>(M);
+    p.K = static_cast<int>(K);
+    p.per = pl.sum_per;
+    p.scale = scale;
+    p.accumulate = accumulate;
+    const dim3 grid(static_cast<unsigned>(pl.sum_ctas),
+                    static_cast<unsigned>((K + 8 * kEmbedThreads - 1) / (8 * kEmbedThreads)));
+    if ((st = launch(embed_sum_kernel, grid, dim3(kEmbedThreads), 0, s, false, p)) != MMF_OK) return st;
+    return launch(embed_join_kernel, grid, dim3(kEmbedThreads), 0, s, false, p);
+}
+
+size_t mmf_mlgru_scan_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D) {
+    if (check_scan_shape(B, T, D) != MMF_OK) return 0;
+    return align256(4 * static_cast<size_t>(B) * static_cast<size_t>((T + kSbSub - 1) / kSbSub) * static_cast<size_t>(D));
+}
+
+int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre, const uint16_t* g_pre, const uint16_t* d_o,
+                       const float* h0, const float* dh_last, int64_t B, int64_t T, int64_t D, uint16_t* df_pre,
+                       uint16_t* dc_pre, uint16_t* dg_pre, float* dh0, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+    mmf_status st = check_scan_shape(B, T, D);
+    if (st != MMF_OK) return st;
+    if (B == 0 || D == 0) return MMF_OK;
+    if (T > 0 && (!f_pre || !c_pre || !g_pre || !d_o || !df_pre || !dc_pre || !dg_pre)) return MMF_ERR_INVALID_ARG;
+    if (T == 0 && !dh0) return MMF_OK;
+    if (!aligned16(f_pre) || !aligned16(c_pre) || !aligned16(g_pre) || !aligned16(d_o) || !aligned16(h0) ||
+        !aligned16(dh_last) || !aligned16(df_pre) || !aligned16(dc_pre) || !aligned16(dg_pre) || !aligned16(dh0) ||
+        !aligned16(workspace))
+        return MMF_ERR_MISALIGNED;
+    const size_t need = mmf_mlgru_scan_bwd_workspace_bytes(B, T, D);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return MMF_ERR_WORKSPACE;
+    DeviceState* dev;
+    if ((st = device_state(&dev)) != MMF_OK) return st;
+    const dim3 grid(static_cast<unsigned>((D + 64 * kSbWarps - 1) / (64 * kSbWarps)), static_cast<unsigned>(B));
+    return launch(mlgru_scan_bwd_kernel, grid, dim3(kSbWarps * 32), 0, static_cast<cudaStream_t>(stream), false, f_pre,
+                  c_pre, g_pre, d_o, h0, dh_last, static_cast<int>(T), static_cast<int>(D),
+                  static_cast<float*>(workspace), df_pre, dc_pre, dg_pre, dh0);
+}
+
+int mmf_adamw_scalars_at(const mmf_adamw_hyper* hyper, mmf_adamw_scalars* out) { return adam_scalars(hyper, out); }
+
+int mmf_adamw_step(const mmf_adamw_tensor* tensors, int count, const mmf_adamw_hyper* hyper,
+                   const mmf_adamw_scalars* scalars, void* stream) {
+    if (count < 0 || (count > 0 && !tensors)) return MMF_ERR_INVALID_ARG;
+    mmf_adamw_scalars sc;
+    mmf_status st = adam_scalars(hyper, &sc);
+    if (st != MMF_OK) return st;
+    for (int i = 0; i < count; ++i)
+        if ((st = adam_check_tensor(tensors[i])) != MMF_OK) return st;
+    if (!aligned16(scalars)) return MMF_ERR_MISALIGNED;
+    if (count == 0) return MMF_OK;
+    if ((st = adam_check_overlap(tensors, count)) != MMF_OK) return st;
+    DeviceState* dev;
+    if ((st = device_state(&dev)) != MMF_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    for (int i = 0; i < count; i += kAdamCap) {
+        const int n = std::min(kAdamCap, count - i);
+        st = n <= 16 ? launch_adamw<16>(tensors, i, n, hyper, sc, scalars, s)
+                     : launch_adamw<kAdamCap>(tensors, i, n, hyper, sc, scalars, s);
+        if (st != MMF_OK) return st;
+    }
+    return MMF_OK;
 }
 
 int mmf_bitlinear_fwd_glu(const uint16_t* g, const uint16_t* u, const float* gamma, float eps,

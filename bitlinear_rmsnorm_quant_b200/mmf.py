@@ -12,7 +12,9 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 import threading
+from dataclasses import dataclass
 
 import torch
 
@@ -47,6 +49,13 @@ SIGNATURES = {
     "mmf_bitlinear_bwd": (_INT, [_P, _P, _P, _F, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
     "mmf_bitlinear_fwd_group": (_INT, [_P, _P, _F, _I64, _I64, _P, _INT, _P, _SZ, C.c_uint, _P]),
     "mmf_bitlinear_fwd_noalloc": (_INT, [_P, _P, _F, _P, _P, _I64, _I64, _I64, _P, _P]),
+    "mmf_embed_fwd": (_INT, [_P, _P, _F, _I64, _I64, _I64, _P, C.c_uint, _P]),
+    "mmf_embed_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "mmf_embed_bwd": (_INT, [_P, _P, _F, _I64, _I64, _I64, _P, _P, _SZ, C.c_uint, _P]),
+    "mmf_mlgru_scan_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "mmf_mlgru_scan_bwd": (_INT, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "mmf_adamw_step": (_INT, [_P, _INT, _P, _P, _P]),
+    "mmf_adamw_scalars_at": (_INT, [_P, _P]),
     "mmf_hbm_copy": (_INT, [_P, _P, _SZ, _P]),
     "mmf_selftest_timeout": (_INT, [C.c_uint64, _P, _P]),
     "mmf_check_async": (_INT, [_P]),
@@ -56,11 +65,20 @@ SIGNATURES = {
 FWD_PDL = 1
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MMF_NOALLOC_SCRATCH_BYTES
 MAX_GROUP = 8
+EMBED_IDS64, EMBED_TABLE_BF16, EMBED_ACCUMULATE = 1, 2, 4
+ADAMW_STATE8, ADAMW_GRAD_BF16 = 1, 2
+ADAMW_BLOCK = 256   # MMF_ADAMW_BLOCK
 
 
 class Projection(C.Structure):
     """mirror of mmf_projection"""
     _fields_ = [("packed", _P), ("scale", _P), ("y", _P), ("N", _I64)]
+
+
+class AdamWHyper(C.Structure):
+    """mirror of mmf_adamw_hyper"""
+    _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_double),
+                ("grad_scale", C.c_double), ("step", _I64), ("seed", C.c_uint64)]
 
 
 class MMFError(RuntimeError):
@@ -273,6 +291,233 @@ def bitlinear_fwd_noalloc(x: torch.Tensor, gamma: torch.Tensor, packed: torch.Te
     check(lib().mmf_bitlinear_fwd_noalloc(x.data_ptr(), gamma.data_ptr(), eps, packed.data_ptr(), scale.data_ptr(),
                                           M, K, N, y.data_ptr(), _stream(stream)), "mmf_bitlinear_fwd_noalloc")
     return y
+
+
+def _on(device: torch.device, stream, call):
+    """call(stream handle) with the tensors' device current and, when a stream is given, with it as torch's
+    current stream, so that what the call allocates belongs to the stream that uses it."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(s):
+            return call(s.cuda_stream)
+
+
+def _like(t: torch.Tensor, dtype, shape, device, name: str):
+    """As _dev, for an argument of a known shape on a known device."""
+    _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _embed_ids(ids: torch.Tensor) -> int:
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
+    _dev(ids, ids.dtype, "ids")
+    return EMBED_IDS64 if ids.dtype == torch.int64 else 0
+
+
+def embed_fwd(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out=None, stream=None):
+    """int32/int64 ids[...] and fp32/bf16 table[V, K] -> bf16 x[..., K] = scale * table[ids]; an id outside
+    [0, V) gives a row of zeros."""
+    flags = _embed_ids(ids)
+    if table.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"table must be torch.float32 or torch.bfloat16, got {table.dtype}")
+    _like(table, table.dtype, table.shape, ids.device, "table")
+    if table.dtype == torch.bfloat16:
+        flags |= EMBED_TABLE_BF16
+    V, K = table.shape
+    if out is not None:
+        _like(out, torch.bfloat16, (*ids.shape, K), ids.device, "out")
+
+    def call(s):
+        x = out if out is not None else torch.empty((*ids.shape, K), dtype=torch.bfloat16, device=ids.device)
+        check(lib().mmf_embed_fwd(ids.data_ptr(), table.data_ptr(), scale, V, ids.numel(), K, x.data_ptr(), flags, s),
+              "mmf_embed_fwd")
+        return x
+
+    return _on(ids.device, stream, call)
+
+
+def embed_bwd_workspace_bytes(V: int, M: int, K: int) -> int:
+    return int(lib().mmf_embed_bwd_workspace_bytes(V, M, K))
+
+
+def embed_bwd(ids: torch.Tensor, dx: torch.Tensor, V: int, scale: float = 1.0, out=None, accumulate: bool = False,
+              workspace=None, stream=None):
+    """Gradient of embed_fwd for its table: int32/int64 ids[...] and bf16 dx[..., K] -> fp32 dtable[V, K];
+    with accumulate the sums are added to `out`, and rows no id names stay as they are."""
+    flags = _embed_ids(ids)
+    K = dx.shape[-1]
+    _like(dx, torch.bfloat16, (*ids.shape, K), ids.device, "dx")
+    if out is not None:
+        _like(out, torch.float32, (V, K), ids.device, "out")
+    if accumulate:
+        if out is None:
+            raise ValueError("accumulate adds to out: out is missing")
+        flags |= EMBED_ACCUMULATE
+    M = ids.numel()
+    need = embed_bwd_workspace_bytes(V, M, K)
+    if workspace is not None:
+        _like(workspace, torch.uint8, workspace.shape, ids.device, "workspace")
+        if workspace.numel() < need:
+            raise ValueError(f"workspace needs {need} bytes")
+
+    def call(s):
+        d = out if out is not None else torch.empty((V, K), dtype=torch.float32, device=ids.device)
+        ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=ids.device)
+        check(lib().mmf_embed_bwd(ids.data_ptr(), dx.data_ptr(), scale, V, M, K, d.data_ptr(), ws.data_ptr(),
+                                  ws.numel(), flags, s), "mmf_embed_bwd")
+        return d
+
+    return _on(ids.device, stream, call)
+
+
+def mlgru_scan_bwd_workspace_bytes(B: int, T: int, D: int) -> int:
+    return int(lib().mmf_mlgru_scan_bwd_workspace_bytes(B, T, D))
+
+
+def mlgru_scan_bwd(f_pre: torch.Tensor, c_pre: torch.Tensor, g_pre: torch.Tensor, d_o: torch.Tensor,
+                   h0: torch.Tensor | None = None, dh_last: torch.Tensor | None = None, outs=None, dh0=None,
+                   workspace=None, stream=None):
+    """Gradient of mlgru_scan: its bf16 [B, T, D] inputs and d_o, the gradient of o (and fp32 [B, D] h0 and
+    dh_last) -> (bf16 df_pre, dc_pre, dg_pre [B, T, D], fp32 dh0 [B, D])."""
+    _dev(f_pre, torch.bfloat16, "f_pre")
+    B, T, D = f_pre.shape
+    dev = f_pre.device
+    for name, t in (("c_pre", c_pre), ("g_pre", g_pre), ("d_o", d_o)):
+        _like(t, torch.bfloat16, f_pre.shape, dev, name)
+    for name, t in (("h0", h0), ("dh_last", dh_last), ("dh0", dh0)):
+        if t is not None:
+            _like(t, torch.float32, (B, D), dev, name)
+    if outs is not None:
+        for name, t in zip(("df_pre", "dc_pre", "dg_pre"), outs, strict=True):
+            _like(t, torch.bfloat16, f_pre.shape, dev, name)
+    need = mlgru_scan_bwd_workspace_bytes(B, T, D)
+    if workspace is not None:
+        _like(workspace, torch.uint8, workspace.shape, dev, "workspace")
+        if workspace.numel() < need:
+            raise ValueError(f"workspace needs {need} bytes")
+
+    def call(s):
+        df, dc, dg = outs if outs is not None else [torch.empty_like(f_pre) for _ in range(3)]
+        dh = dh0 if dh0 is not None else torch.empty((B, D), dtype=torch.float32, device=dev)
+        ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=dev)
+        check(lib().mmf_mlgru_scan_bwd(f_pre.data_ptr(), c_pre.data_ptr(), g_pre.data_ptr(), d_o.data_ptr(),
+                                       h0.data_ptr() if h0 is not None else None,
+                                       dh_last.data_ptr() if dh_last is not None else None, B, T, D, df.data_ptr(),
+                                       dc.data_ptr(), dg.data_ptr(), dh.data_ptr(), ws.data_ptr(), ws.numel(), s),
+              "mmf_mlgru_scan_bwd")
+        return df, dc, dg, dh
+
+    return _on(dev, stream, call)
+
+
+@dataclass(slots=True)
+class AdamWTensor:
+    """One tensor of an AdamW step: fp32 p, its fp32 or bf16 gradient g, and its moments m, v (adamw_state),
+    fp32 or float8_e4m3fn / float8_e5m2 with their blocks' scales; p_bf16 receives a bf16 copy of the new p."""
+    p: torch.Tensor
+    g: torch.Tensor
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+    p_bf16: torch.Tensor | None = None
+    weight_decay: float = 0.0
+
+
+def adamw_state(p: torch.Tensor, bits: int = 32) -> dict:
+    """Fresh moments for p in 32 or 8 bits, as AdamWTensor's keyword arguments."""
+    if bits == 32:
+        return {"m": torch.zeros_like(p), "v": torch.zeros_like(p)}
+    if bits != 8:
+        raise ValueError(f"bits must be 32 or 8, got {bits}")
+    blocks = -(-p.numel() // ADAMW_BLOCK)
+    return {"m": torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(torch.float8_e4m3fn),
+            "v": torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(torch.float8_e5m2),
+            "m_scale": torch.zeros(blocks, dtype=torch.float32, device=p.device),
+            "v_scale": torch.zeros(blocks, dtype=torch.float32, device=p.device)}
+
+
+_ADAMW_DESC = struct.Struct("<7QqfI")   # mmf_adamw_tensor
+
+
+def _adamw_describe(t: AdamWTensor, device, buf, at: int) -> None:
+    p, g, m, v, ms, vs, pb = t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.p_bf16
+    n = p.numel()
+    flags = 0
+    if g.dtype == torch.bfloat16:
+        flags = ADAMW_GRAD_BF16
+    elif g.dtype != torch.float32:
+        raise TypeError(f"g must be torch.float32 or torch.bfloat16, got {g.dtype}")
+    if m.dtype == torch.float8_e4m3fn:
+        flags |= ADAMW_STATE8
+        if v.dtype != torch.float8_e5m2:
+            raise TypeError(f"v must be torch.float8_e5m2 beside an 8-bit m, got {v.dtype}")
+        blocks = -(-n // ADAMW_BLOCK)
+        for name, s in (("m_scale", ms), ("v_scale", vs)):
+            if s is None:
+                raise ValueError(f"{name} is missing: 8-bit moments need their scales")
+            _like(s, torch.float32, (blocks,), device, name)
+    elif m.dtype != torch.float32 or v.dtype != torch.float32 or ms is not None or vs is not None:
+        raise TypeError("m and v must be torch.float32, or torch.float8_e4m3fn and torch.float8_e5m2 with their scales")
+    if p.dtype != torch.float32:
+        raise TypeError(f"p must be torch.float32, got {p.dtype}")
+    if pb is not None:
+        _like(pb, torch.bfloat16, p.shape, device, "p_bf16")
+    for name, x in (("p", p), ("g", g), ("m", m), ("v", v)):
+        if x.device != device:
+            raise ValueError(f"{name} must be on {device}, got {x.device}")
+        if x.numel() != n or not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous, with as many elements as p")
+    _ADAMW_DESC.pack_into(buf, at, p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(),
+                          ms.data_ptr() if ms is not None else 0, vs.data_ptr() if vs is not None else 0,
+                          pb.data_ptr() if pb is not None else 0, n, t.weight_decay, flags)
+
+
+def _adamw_hyper(step, lr, beta1, beta2, eps, grad_scale, seed) -> AdamWHyper:
+    return AdamWHyper(lr, beta1, beta2, eps, grad_scale, step, seed)
+
+
+def adamw_scalars(step: int, lr: float, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8,
+                  grad_scale: float = 1.0, seed: int = 0) -> torch.Tensor:
+    """A step's scalars as 32 bytes on the host (pinned when there is a GPU): copy them into the device buffer
+    that a captured adamw_step was given as `scalars` before each replay."""
+    out = torch.zeros(32, dtype=torch.uint8, pin_memory=torch.cuda.is_available())
+    hyper = _adamw_hyper(step, lr, beta1, beta2, eps, grad_scale, seed)
+    check(lib().mmf_adamw_scalars_at(C.byref(hyper), out.data_ptr()), "mmf_adamw_scalars_at")
+    return out
+
+
+def adamw_step(tensors, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8,
+               grad_scale: float = 1.0, seed: int = 0, scalars: torch.Tensor | None = None, stream=None) -> None:
+    """One AdamW step over a sequence of AdamWTensor, in place; `step` counts from 1.  With `scalars` (uint8[32]
+    on the device, see adamw_scalars) the kernel takes lr, the bias corrections, grad_scale and seed from there."""
+    tensors = list(tensors)
+    if not tensors:
+        return
+    device = tensors[0].p.device
+    if device.type != "cuda":
+        raise ValueError("p must be a CUDA tensor")
+    buf = bytearray(_ADAMW_DESC.size * len(tensors))
+    for i, t in enumerate(tensors):
+        _adamw_describe(t, device, buf, i * _ADAMW_DESC.size)
+    if scalars is not None:
+        _like(scalars, torch.uint8, (32,), device, "scalars")
+    hyper = _adamw_hyper(step, lr, beta1, beta2, eps, grad_scale, seed)
+    desc = (C.c_char * len(buf)).from_buffer(buf)
+
+    def call(s):
+        check(lib().mmf_adamw_step(C.addressof(desc), len(tensors), C.addressof(hyper),
+                                   scalars.data_ptr() if scalars is not None else None, s), "mmf_adamw_step")
+
+    _on(device, stream, call)
 
 
 def hbm_copy(src: torch.Tensor, dst: torch.Tensor, stream=None):

@@ -224,6 +224,141 @@ int mmf_bitlinear_bwd(const uint16_t* dy, const uint16_t* x, const float* gamma,
                       float* dgamma, float* dW, void* workspace,
                       size_t workspace_bytes, void* stream);
 
+/*
+ * mmf_embed_fwd -- the model's embedding: lookup with scaling, the x of its
+ * first layer (nothing on the pages fixes it; the plain definition):
+ *   x[m][k] = bf16_rn(scale * table[ids[m]][k])          (the product in fp32)
+ * ids: int32 [M], or int64 [M] with MMF_EMBED_IDS64; table: fp32 [V][K], or
+ * bf16 [V][K] with MMF_EMBED_TABLE_BF16; x: bf16 [M][K].  An id outside
+ * [0, V) (the usual -1 of a padded place) gives a row of zeros.  K % 8 == 0,
+ * 8 <= K <= 65536, V < 2^31 - 1, M as above; scale finite.  x must not overlap
+ * the inputs.
+ */
+#define MMF_EMBED_IDS64 1u       /* ids are int64 (else int32) */
+#define MMF_EMBED_TABLE_BF16 2u  /* mmf_embed_fwd: the table is bf16 (else fp32) */
+#define MMF_EMBED_ACCUMULATE 4u  /* mmf_embed_bwd: add to dtable (else overwrite it) */
+int mmf_embed_fwd(const void* ids, const void* table, float scale, int64_t V,
+                  int64_t M, int64_t K, uint16_t* x, unsigned flags, void* stream);
+
+/*
+ * mmf_embed_bwd -- gradient of mmf_embed_fwd for the table:
+ *   dtable[v][k] = scale * sum over the tokens m with ids[m] = v of dx[m][k]
+ * in fp32; with MMF_EMBED_ACCUMULATE the sum is added to dtable[v][k], and rows
+ * no token names are not touched (without the flag they become zeros).  The
+ * tokens are sorted by id and each row's are added in their order in a fixed
+ * grouping: the same ids and dx give the same bits on every run.  A place whose
+ * id is outside [0, V) takes no part.
+ * ids as above; dx: bf16 [M][K] (as from mmf_bitlinear_bwd); dtable: fp32
+ * [V][K].  workspace: at least mmf_embed_bwd_workspace_bytes(V, M, K) bytes,
+ * no initialisation needed.  M == 0 without the flag writes zeros.
+ */
+size_t mmf_embed_bwd_workspace_bytes(int64_t V, int64_t M, int64_t K);
+int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V,
+                  int64_t M, int64_t K, float* dtable, void* workspace,
+                  size_t workspace_bytes, unsigned flags, void* stream);
+
+/*
+ * mmf_mlgru_scan_bwd -- gradient of mmf_mlgru_scan.  The states are recomputed
+ * from the pre-activations; nothing of the forward has to be kept but its
+ * inputs.  With f, c, g, h as there and s = sigma(c_pre), from dh_T = dh_last
+ * (0 when NULL) + do_T g_T, the tokens taken backwards:
+ *   dh_t   = do_t g_t + f_{t+1} dh_{t+1},          dh0 = f_1 dh_1
+ *   df_pre = bf16_rn(dh_t (h_{t-1} - c_t) f (1 - f))
+ *   dc_pre = bf16_rn(dh_t (1 - f) s (1 + c_pre (1 - s)))
+ *   dg_pre = bf16_rn(do h_t g (1 - g))
+ * in fp32.  f_pre, c_pre, g_pre, d_o (the gradient of o) and the outputs
+ * df_pre, dc_pre, dg_pre: bf16 [B][T][D]; h0, dh_last (may be NULL) and dh0
+ * (may be NULL: not wanted): fp32 [B][D].  Sizes as mmf_mlgru_scan.  The
+ * outputs must not overlap the inputs or one another.  T = 0 copies dh_last
+ * (or zeros) to dh0.  workspace: at least
+ * mmf_mlgru_scan_bwd_workspace_bytes(B, T, D) bytes, no initialisation needed.
+ */
+size_t mmf_mlgru_scan_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D);
+int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre,
+                       const uint16_t* g_pre, const uint16_t* d_o,
+                       const float* h0, const float* dh_last, int64_t B,
+                       int64_t T, int64_t D, uint16_t* df_pre, uint16_t* dc_pre,
+                       uint16_t* dg_pre, float* dh0, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * mmf_adamw_step -- one AdamW step over `count` tensors at once (the pages name
+ * no optimiser; the plain definition, decoupled weight decay).  Per element:
+ *   g' = g * grad_scale
+ *   m  = beta1 * m + (1 - beta1) * g'
+ *   v  = beta2 * v + (1 - beta2) * g'^2
+ *   p  = p * (1 - lr * weight_decay)
+ *        - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32 (m and v as separately rounded products and sums, so their bits are
+ * those of the elementwise fp32 operations).  p: fp32 [n], updated in place;
+ * p_bf16: bf16 [n] copy of the new p, or NULL; g: fp32 [n], or bf16 [n] with
+ * MMF_ADAMW_GRAD_BF16.
+ * m, v: fp32 [n], or with MMF_ADAMW_STATE8 8-bit floats [n] in blocks of
+ * MMF_ADAMW_BLOCK consecutive elements (the last block may be short), m as
+ * e4m3 codes and v as e5m2 codes, the values code * m_scale[block] and
+ * code * v_scale[block] (fp32 [ceil(n / 256)], powers of two).  With 2^e <=
+ * the block's largest |m| < 2^(e+1), e taken as at least -90, m_scale =
+ * 2^(e-7), and v_scale = 2^(e-14) likewise.  The codes are rounded up or down
+ * at random, with the right mean: 16 bits per moment from draw floor(i / 2) of
+ * the SplitMix64 stream (seed, index of the tensor in the call) for element i;
+ * p is updated with the moments before they are rounded.  |m| below the
+ * smallest normal code becomes 0; a positive v is kept at least at the
+ * smallest normal code.  A block in which a moment is 2^127 or more, infinite
+ * or NaN reads as NaN from then on.  All zeros are the fresh states of either
+ * kind.
+ *
+ * tensors: HOST array, read during the call only; n == 0 is skipped (its
+ * pointers may be NULL).  p, p_bf16, m, v, m_scale and v_scale of one call must
+ * not overlap one another (checked, MMF_ERR_INVALID_ARG) nor any g.  Launches
+ * one kernel per 256 tensors.
+ *
+ * hyper: HOST struct, read during the call only.  0 <= beta < 1, eps > 0,
+ * lr >= 0, step >= 1 (the count that includes this step), everything finite.
+ * scalars: NULL, or a DEVICE copy (16-byte aligned) of what
+ * mmf_adamw_scalars_at fills: the kernel then takes lr, the bias corrections,
+ * grad_scale and the seed from there and not from hyper, so a captured graph
+ * takes each replay's values from memory (a gradient-clipping factor computed
+ * on the device may be written there too).
+ */
+#define MMF_ADAMW_STATE8 1u     /* m, v in 8 bits */
+#define MMF_ADAMW_GRAD_BF16 2u  /* g is bf16 (else fp32) */
+#define MMF_ADAMW_BLOCK 256     /* elements that share m_scale and v_scale */
+
+typedef struct mmf_adamw_tensor {
+    float* p;
+    const void* g;
+    void* m;
+    void* v;
+    float* m_scale;     /* NULL without MMF_ADAMW_STATE8 */
+    float* v_scale;
+    uint16_t* p_bf16;   /* may be NULL */
+    int64_t n;
+    float weight_decay; /* >= 0 */
+    unsigned flags;
+} mmf_adamw_tensor;
+
+typedef struct mmf_adamw_hyper {
+    double lr, beta1, beta2, eps, grad_scale;
+    int64_t step;
+    uint64_t seed;
+} mmf_adamw_hyper;
+
+typedef struct mmf_adamw_scalars {
+    float lr;
+    float alpha;         /* lr / (1 - beta1^step) */
+    float inv_sqrt_bc2;  /* 1 / sqrt(1 - beta2^step) */
+    float grad_scale;
+    uint64_t seed;
+    uint64_t reserved;
+} mmf_adamw_scalars;
+
+int mmf_adamw_step(const mmf_adamw_tensor* tensors, int count,
+                   const mmf_adamw_hyper* hyper,
+                   const mmf_adamw_scalars* scalars, void* stream);
+
+/* Fills *out (HOST) with the scalars of a step; launches nothing. */
+int mmf_adamw_scalars_at(const mmf_adamw_hyper* hyper, mmf_adamw_scalars* out);
+
 /* Flags of mmf_bitlinear_fwd_group. */
 #define MMF_FWD_PDL 1u   /* launch as a programmatic dependent of the kernel before it on the stream (see below) */
 #define MMF_MAX_GROUP 8  /* projections per mmf_bitlinear_fwd_group call */
