@@ -632,6 +632,49 @@ mmf_status check_scan_shape(int64_t B, int64_t T, int64_t D) {
     return MMF_OK;
 }
 
+// How the recurrence's gradient splits a sequence: segments of whole
+// kSbSub-token steps, as many as give the GPU kSbItems warps to run, but of at
+// least kSbMinTokens tokens, since each folds the maps of all others.
+constexpr int64_t kSbItems = 148 * 32;
+constexpr int64_t kSbMinTokens = 64;
+
+struct ScanBwdPlan {
+    int tiles, subs, subs_per_seg, segments;
+};
+
+ScanBwdPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D) {
+    ScanBwdPlan pl;
+    pl.tiles = static_cast<int>((D + 63) / 64);
+    pl.subs = static_cast<int>((T + kSbSub - 1) / kSbSub);
+    const int64_t want = (kSbItems + B * pl.tiles - 1) / (B * pl.tiles);
+    const int64_t per = std::max((pl.subs + want - 1) / want, kSbMinTokens / kSbSub);
+    pl.subs_per_seg = static_cast<int>(std::min<int64_t>(per, pl.subs));
+    pl.segments = (pl.subs + pl.subs_per_seg - 1) / pl.subs_per_seg;
+    return pl;
+}
+
+struct ScanBwdWorkspace {
+    float4* part;
+    float4* seg;
+    float2* seg_r;
+    size_t bytes;
+};
+
+ScanBwdWorkspace carve_scan_bwd(void* ws, const ScanBwdPlan& pl, int64_t B, int64_t D) {
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    const size_t row = static_cast<size_t>(B) * static_cast<size_t>(D) / 2;
+    ScanBwdWorkspace w;
+    size_t at = 0;
+    w.part = reinterpret_cast<float4*>(b + at);
+    at += align256(row * pl.subs * sizeof(float4));
+    w.seg = reinterpret_cast<float4*>(b + at);
+    at += align256(row * pl.segments * sizeof(float4));
+    w.seg_r = reinterpret_cast<float2*>(b + at);
+    at += align256(row * pl.segments * sizeof(float2));
+    w.bytes = at;
+    return w;
+}
+
 // ---------------------------------------------------------------------------
 // AdamW
 // ---------------------------------------------------------------------------
@@ -1124,8 +1167,8 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, i
 }
 
 size_t mmf_mlgru_scan_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D) {
-    if (check_scan_shape(B, T, D) != MMF_OK) return 0;
-    return align256(4 * static_cast<size_t>(B) * static_cast<size_t>((T + kSbSub - 1) / kSbSub) * static_cast<size_t>(D));
+    if (check_scan_shape(B, T, D) != MMF_OK || B == 0 || T == 0 || D == 0) return 0;
+    return carve_scan_bwd(nullptr, scan_bwd_plan(B, T, D), B, D).bytes;
 }
 
 int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre, const uint16_t* g_pre, const uint16_t* d_o,
@@ -1145,10 +1188,39 @@ int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre, const uint1
     if (need > 0 && (!workspace || workspace_bytes < need)) return MMF_ERR_WORKSPACE;
     DeviceState* dev;
     if ((st = device_state(&dev)) != MMF_OK) return st;
-    const dim3 grid(static_cast<unsigned>((D + 64 * kSbWarps - 1) / (64 * kSbWarps)), static_cast<unsigned>(B));
-    return launch(mlgru_scan_bwd_kernel, grid, dim3(kSbWarps * 32), 0, static_cast<cudaStream_t>(stream), false, f_pre,
-                  c_pre, g_pre, d_o, h0, dh_last, static_cast<int>(T), static_cast<int>(D),
-                  static_cast<float*>(workspace), df_pre, dc_pre, dg_pre, dh0);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        const size_t bytes = 4 * static_cast<size_t>(B) * static_cast<size_t>(D);
+        const cudaError_t e = dh_last ? cudaMemcpyAsync(dh0, dh_last, bytes, cudaMemcpyDeviceToDevice, s)
+                                      : cudaMemsetAsync(dh0, 0, bytes, s);
+        return e == cudaSuccess ? MMF_OK : MMF_ERR_CUDA;
+    }
+    const ScanBwdPlan pl = scan_bwd_plan(B, T, D);
+    const ScanBwdWorkspace w = carve_scan_bwd(workspace, pl, B, D);
+    ScanBwdParams p{};
+    p.f_pre = f_pre;
+    p.c_pre = c_pre;
+    p.g_pre = g_pre;
+    p.d_o = d_o;
+    p.h0 = h0;
+    p.dh_last = dh_last;
+    p.df_pre = df_pre;
+    p.dc_pre = dc_pre;
+    p.dg_pre = dg_pre;
+    p.dh0 = dh0;
+    p.part = w.part;
+    p.seg = w.seg;
+    p.seg_r = w.seg_r;
+    p.T = static_cast<int>(T);
+    p.D = static_cast<int>(D);
+    p.S = pl.segments;
+    p.subs = pl.subs;
+    p.subs_per_seg = pl.subs_per_seg;
+    p.tiles = pl.tiles;
+    p.items = B * pl.segments * static_cast<int64_t>(pl.tiles);
+    const dim3 grid(static_cast<unsigned>((p.items + kSbWarps - 1) / kSbWarps)), block(kSbWarps * 32);
+    if ((st = launch(mlgru_scan_bwd_maps_kernel, grid, block, 0, s, false, p)) != MMF_OK) return st;
+    return launch(mlgru_scan_bwd_kernel, grid, block, 0, s, true, p);
 }
 
 int mmf_adamw_scalars_at(const mmf_adamw_hyper* hyper, mmf_adamw_scalars* out) { return adam_scalars(hyper, out); }

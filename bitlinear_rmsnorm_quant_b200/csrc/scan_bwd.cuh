@@ -9,121 +9,240 @@
 //   dc_pre = dh_t (1 - f) s (1 + c_pre (1 - s)).
 // 1 - sigma(v) is taken as e^-v sigma(v), which keeps its precision where
 // sigma(v) is close to 1.
+//
+// Both recurrences are linear, so a run of tokens acts on them as
+//   h -> A h + P  (forward)  and  dh -> A dh + R  (backward), A = prod f,
+// and P and R both come out of one forward walk (R = sum A_t do_t g_t with A_t
+// the product up to token t).  The tokens of a sequence are split into
+// segments; mlgru_scan_bwd_maps_kernel walks each and leaves its (A, P, R),
+// and on the way the (A, P) of the tokens before every kSbSub-th one.
+// mlgru_scan_bwd_kernel folds the segments before and behind its own into the
+// state and the gradient that enter it, and takes it backwards, kSbSub tokens
+// at a time: their gates once, their states forward from the kept map, their
+// gradients backward.  A warp works alone, on 64 channels (a bf16 pair per
+// lane) of one segment: no barriers, and any number of channels, segments and
+// sequences fills the GPU alike.
 #pragma once
 #include "common.cuh"
 #include "scan.cuh"
 
 namespace mmf {
 
-// max(v, kScanClamp) that passes a NaN on (fmaxf would return the clamp).
-__device__ __forceinline__ float clamp_nan(float v) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(kScanClamp));
+constexpr int kSbSub = 8;      // tokens taken backwards at a time
+constexpr int kSbWarps = 4;    // warps per CTA, each on a segment of its own
+
+// A channel pair's fp32 values, computed two at a time (packed fp32 pairs).
+typedef unsigned long long f2;
+
+__device__ __forceinline__ f2 f2_make(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
     return r;
 }
+__device__ __forceinline__ float2 f2_get(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 f2_set(float v) { return f2_make(v, v); }
 
-// e^-v, 1 + e^-v of the clamped pre-activation
-__device__ __forceinline__ float sig_exp(float v) { return ex2_ftz(-kLog2e * clamp_nan(v)); }
-
-constexpr int kSbSub = 8;      // tokens between two kept states
-constexpr int kSbWarps = 4;    // warps per CTA, each on 64 channels of its own
-
-// h -> f h + (1 - f) c of one token and channel
-__device__ __forceinline__ float scan_step(float fp, float cp, float h) {
-    const float ef = sig_exp(fp), ec = sig_exp(cp);
-    const float df = 1.0f + ef, dc = 1.0f + ec;
-    const float r = rcp_ftz(df * dc);
-    const float f = r * dc;
-    return fmaf(f, h, ef * f * (cp * (r * df)));
+// a bf16 pair -> fp32 pair
+__device__ __forceinline__ f2 f2_bf16(uint32_t w) {
+    return f2_make(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+// a bf16 pair raised to at least kScanClamp (-28 is a bf16 value); a NaN stays
+__device__ __forceinline__ uint32_t clamp_bf16x2(uint32_t w) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0xC1E0C1E0u));
+    return r;
+}
+__device__ __forceinline__ f2 f2_exp_neg(f2 v) {  // e^-v
+    const float2 a = f2_get(f2_mul(v, f2_set(-kLog2e)));
+    return f2_make(ex2_ftz(a.x), ex2_ftz(a.y));
+}
+__device__ __forceinline__ uint32_t f2_to_bf16(f2 v) {
+    const float2 a = f2_get(v);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(a.x, a.y);
+    return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// A warp takes 64 channels (a bf16 pair per lane) of one sequence: forward
-// through the tokens, keeping the state before every kSbSub-th token in `kept`
-// ([B][ceil(T / kSbSub)][D] fp32), then backwards, kSbSub tokens at a time,
-// their states recomputed from the kept one.
-__global__ void __launch_bounds__(kSbWarps * 32) mlgru_scan_bwd_kernel(
-    const uint16_t* __restrict__ f_pre, const uint16_t* __restrict__ c_pre, const uint16_t* __restrict__ g_pre,
-    const uint16_t* __restrict__ d_o, const float* __restrict__ h0, const float* __restrict__ dh_last, int T, int D,
-    float* __restrict__ kept, uint16_t* __restrict__ df_pre, uint16_t* __restrict__ dc_pre,
-    uint16_t* __restrict__ dg_pre, float* __restrict__ dh0) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t b = blockIdx.y;
-    const int k = (blockIdx.x * kSbWarps + warp) * 64 + 2 * lane;  // this lane's channels k, k + 1
-    if (k >= D) return;                                            // D is even, so k + 1 < D too
-    const int subs = (T + kSbSub - 1) / kSbSub;
-    const int64_t base = b * T * static_cast<int64_t>(D) + k;
-    float* keep = kept + b * subs * static_cast<int64_t>(D) + k;
-    float2 h = make_float2(0.0f, 0.0f);
-    if (h0) h = *reinterpret_cast<const float2*>(h0 + b * D + k);
-    for (int t = 0; t < T; ++t) {
-        if (t % kSbSub == 0) *reinterpret_cast<float2*>(keep + (t / kSbSub) * static_cast<int64_t>(D)) = h;
-        float fp0, fp1, cp0, cp1;
-        const int64_t at = base + t * static_cast<int64_t>(D);
-        bf16x2_to_f(__ldg(reinterpret_cast<const uint32_t*>(f_pre + at)), fp0, fp1);
-        bf16x2_to_f(__ldg(reinterpret_cast<const uint32_t*>(c_pre + at)), cp0, cp1);
-        h.x = scan_step(fp0, cp0, h.x);
-        h.y = scan_step(fp1, cp1, h.y);
+// The gates of one token from its (clamped) pre-activations: one reciprocal
+// gives all three sigmoids (scan.cuh).
+struct ScanGates {
+    f2 cp, ef, ec, eg, f, s, g;
+    __device__ __forceinline__ ScanGates(uint32_t wf, uint32_t wc, uint32_t wg) {
+        cp = f2_bf16(clamp_bf16x2(wc));
+        ef = f2_exp_neg(f2_bf16(clamp_bf16x2(wf)));
+        ec = f2_exp_neg(cp);
+        eg = f2_exp_neg(f2_bf16(clamp_bf16x2(wg)));
+        const f2 one = f2_set(1.0f);
+        const f2 df = f2_add(one, ef), dc = f2_add(one, ec), dg = f2_add(one, eg);
+        const f2 dfc = f2_mul(df, dc);
+        const float2 all = f2_get(f2_mul(dfc, dg));
+        const f2 r = f2_make(rcp_ftz(all.x), rcp_ftz(all.y));
+        const f2 rg = f2_mul(r, dg);  // 1 / (df dc)
+        f = f2_mul(rg, dc);
+        s = f2_mul(rg, df);
+        g = f2_mul(r, dfc);
     }
-    float dh[2] = {0.0f, 0.0f};
-    if (dh_last) {
-        const float2 v = *reinterpret_cast<const float2*>(dh_last + b * D + k);
-        dh[0] = v.x;
-        dh[1] = v.y;
+};
+
+struct ScanBwdParams {
+    const uint16_t *f_pre, *c_pre, *g_pre, *d_o;
+    const float *h0, *dh_last;
+    uint16_t *df_pre, *dc_pre, *dg_pre;
+    float* dh0;
+    float4* part;  // [B][subs][D / 2] (A, A, P, P) of the segment's tokens before each kSbSub-th
+    float4* seg;   // [B][S][D / 2] (A, A, P, P) of a segment
+    float2* seg_r; // [B][S][D / 2] R of a segment
+    int T, D, S, subs, subs_per_seg, tiles;
+    int64_t items; // B * S * tiles
+};
+
+// Which segment a warp takes, and where its data begins.
+struct ScanItem {
+    int64_t b;
+    int seg, k;      // k: this lane's first channel
+    bool valid;      // D is even, so k + 1 < D too
+    __device__ __forceinline__ ScanItem(const ScanBwdParams& p, int64_t item) {
+        const int tile = static_cast<int>(item % p.tiles);
+        const int64_t bs = item / p.tiles;
+        seg = static_cast<int>(bs % p.S);
+        b = bs / p.S;
+        k = tile * 64 + 2 * (threadIdx.x & 31);
+        valid = k < p.D;
     }
-    for (int s = subs - 1; s >= 0; --s) {
-        const float2 hv = *reinterpret_cast<const float2*>(keep + s * static_cast<int64_t>(D));
-        float hp[kSbSub + 1][2];   // hp[i]: the state before token i of these
-        hp[0][0] = hv.x;
-        hp[0][1] = hv.y;
-        const int n = min(kSbSub, T - s * kSbSub);
-        const int64_t at0 = base + static_cast<int64_t>(s) * kSbSub * D;
-        uint32_t rf[kSbSub], rc[kSbSub];
+};
+
+__device__ __forceinline__ uint32_t ld_pair(const uint16_t* p) { return __ldg(reinterpret_cast<const uint32_t*>(p)); }
+
+__global__ void __launch_bounds__(kSbWarps * 32) mlgru_scan_bwd_maps_kernel(const ScanBwdParams p) {
+    pdl_launch_dependents();
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kSbWarps + (threadIdx.x >> 5);
+    if (item >= p.items) return;
+    const ScanItem it(p, item);
+    if (!it.valid) return;
+    const int sub0 = it.seg * p.subs_per_seg, sub1 = min(p.subs, sub0 + p.subs_per_seg);
+    const int64_t half = p.D / 2;
+    f2 A = f2_set(1.0f), P = f2_set(0.0f), R = f2_set(0.0f);
+    for (int sub = sub0; sub < sub1; ++sub) {
+        const int t0 = sub * kSbSub;
+        const int64_t at = (it.b * p.T + t0) * p.D + it.k;
+        const float2 a = f2_get(A), q = f2_get(P);
+        p.part[(it.b * p.subs + sub) * half + it.k / 2] = make_float4(a.x, a.y, q.x, q.y);
+        const int n = min(kSbSub, p.T - t0);
+        uint32_t wf[kSbSub], wc[kSbSub], wg[kSbSub], wd[kSbSub];
 #pragma unroll
         for (int i = 0; i < kSbSub; ++i) {
-            if (i < n) {
-                rf[i] = __ldg(reinterpret_cast<const uint32_t*>(f_pre + at0 + i * static_cast<int64_t>(D)));
-                rc[i] = __ldg(reinterpret_cast<const uint32_t*>(c_pre + at0 + i * static_cast<int64_t>(D)));
-                float fp[2], cp[2];
-                bf16x2_to_f(rf[i], fp[0], fp[1]);
-                bf16x2_to_f(rc[i], cp[0], cp[1]);
-                hp[i + 1][0] = scan_step(fp[0], cp[0], hp[i][0]);
-                hp[i + 1][1] = scan_step(fp[1], cp[1], hp[i][1]);
-            } else {
-                rf[i] = rc[i] = 0;
-                hp[i + 1][0] = hp[i + 1][1] = 0.0f;
-            }
+            const int64_t o = at + static_cast<int64_t>(i) * p.D;
+            const bool there = i < n;
+            wf[i] = there ? ld_pair(p.f_pre + o) : 0u;
+            wc[i] = there ? ld_pair(p.c_pre + o) : 0u;
+            wg[i] = there ? ld_pair(p.g_pre + o) : 0u;
+            wd[i] = there ? ld_pair(p.d_o + o) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < kSbSub; ++i) {
+            if (i >= n) break;
+            const ScanGates t(wf[i], wc[i], wg[i]);
+            A = f2_mul(A, t.f);
+            P = f2_fma(t.f, P, f2_mul(f2_mul(t.ef, t.f), f2_mul(t.cp, t.s)));
+            R = f2_fma(A, f2_mul(f2_bf16(wd[i]), t.g), R);
+        }
+    }
+    const float2 a = f2_get(A), q = f2_get(P), r = f2_get(R);
+    const int64_t to = (it.b * p.S + it.seg) * half + it.k / 2;
+    p.seg[to] = make_float4(a.x, a.y, q.x, q.y);
+    p.seg_r[to] = r;
+}
+
+__global__ void __launch_bounds__(kSbWarps * 32, 4) mlgru_scan_bwd_kernel(const ScanBwdParams p) {
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kSbWarps + (threadIdx.x >> 5);
+    if (item >= p.items) return;
+    // the last segments first: the maps kernel has just read them
+    const ScanItem it(p, p.items - 1 - item);
+    if (!it.valid) return;
+    const int sub0 = it.seg * p.subs_per_seg, sub1 = min(p.subs, sub0 + p.subs_per_seg);
+    const int64_t half = p.D / 2;
+    f2 h = f2_set(0.0f), dh = f2_set(0.0f);
+    if (p.h0) h = *reinterpret_cast<const f2*>(p.h0 + it.b * p.D + it.k);
+    if (p.dh_last) dh = *reinterpret_cast<const f2*>(p.dh_last + it.b * p.D + it.k);
+    pdl_wait();
+    {
+        const float4* seg = p.seg + it.b * p.S * half + it.k / 2;
+        const float2* seg_r = p.seg_r + it.b * p.S * half + it.k / 2;
+#pragma unroll 4
+        for (int s = 0; s < it.seg; ++s) {
+            const float4 m = seg[s * half];
+            h = f2_fma(f2_make(m.x, m.y), h, f2_make(m.z, m.w));
+        }
+#pragma unroll 4
+        for (int s = p.S - 1; s > it.seg; --s) {
+            const float4 m = seg[s * half];
+            const float2 r = seg_r[s * half];
+            dh = f2_fma(f2_make(m.x, m.y), dh, f2_make(r.x, r.y));
+        }
+    }
+    for (int sub = sub1 - 1; sub >= sub0; --sub) {
+        const int t0 = sub * kSbSub;
+        const int64_t at = (it.b * p.T + t0) * p.D + it.k;
+        const int n = min(kSbSub, p.T - t0);
+        const float4 m = p.part[(it.b * p.subs + sub) * half + it.k / 2];
+        uint32_t wf[kSbSub], wc[kSbSub], wg[kSbSub], wd[kSbSub];
+#pragma unroll
+        for (int i = 0; i < kSbSub; ++i) {
+            const int64_t o = at + static_cast<int64_t>(i) * p.D;
+            const bool there = i < n;
+            wf[i] = there ? ld_pair(p.f_pre + o) : 0u;
+            wc[i] = there ? ld_pair(p.c_pre + o) : 0u;
+            wg[i] = there ? ld_pair(p.g_pre + o) : 0u;
+            wd[i] = there ? ld_pair(p.d_o + o) : 0u;
+        }
+        f2 hs = f2_fma(f2_make(m.x, m.y), h, f2_make(m.z, m.w));  // the state before these tokens
+        // of each token: what dh is multiplied with for df_pre, dc_pre and the token before, and do g
+        f2 xf[kSbSub], xc[kSbSub], fg[kSbSub], dg[kSbSub];
+#pragma unroll
+        for (int i = 0; i < kSbSub; ++i) {
+            if (i >= n) break;
+            const ScanGates t(wf[i], wc[i], wg[i]);
+            const f2 one = f2_set(1.0f);
+            const f2 d_o = f2_bf16(wd[i]);
+            const f2 omf = f2_mul(t.ef, t.f);   // 1 - f
+            const f2 c = f2_mul(t.cp, t.s);
+            xf[i] = f2_mul(f2_fma(c, f2_set(-1.0f), hs), f2_mul(t.f, omf));
+            xc[i] = f2_mul(omf, f2_mul(t.s, f2_fma(t.cp, f2_mul(t.ec, t.s), one)));
+            hs = f2_fma(t.f, hs, f2_mul(omf, c));
+            fg[i] = t.f;
+            dg[i] = f2_mul(d_o, t.g);
+            *reinterpret_cast<uint32_t*>(p.dg_pre + at + static_cast<int64_t>(i) * p.D) =
+                f2_to_bf16(f2_mul(f2_mul(dg[i], hs), f2_mul(t.eg, t.g)));
         }
 #pragma unroll
         for (int i = kSbSub - 1; i >= 0; --i) {
-            if (i < n) {
-                const int64_t at = at0 + i * static_cast<int64_t>(D);
-                float fp[2], cp[2], gp[2], dov[2], ov[3][2];
-                bf16x2_to_f(rf[i], fp[0], fp[1]);
-                bf16x2_to_f(rc[i], cp[0], cp[1]);
-                bf16x2_to_f(__ldg(reinterpret_cast<const uint32_t*>(g_pre + at)), gp[0], gp[1]);
-                bf16x2_to_f(__ldg(reinterpret_cast<const uint32_t*>(d_o + at)), dov[0], dov[1]);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float ef = sig_exp(fp[j]), ec = sig_exp(cp[j]), eg = sig_exp(gp[j]);
-                    const float df = 1.0f + ef, dc = 1.0f + ec, dg = 1.0f + eg;
-                    const float dfc = df * dc;
-                    const float r = rcp_ftz(dfc * dg);
-                    const float rg = r * dg;                      // 1 / (df dc)
-                    const float f = rg * dc, sc = rg * df, g = r * dfc;
-                    const float omf = ef * f, omc = ec * sc, omg = eg * g;  // 1 - f, 1 - sigma(c_pre), 1 - g
-                    const float d = fmaf(dov[j], g, dh[j]);
-                    ov[2][j] = dov[j] * hp[i + 1][j] * (g * omg);
-                    ov[0][j] = d * (hp[i][j] - cp[j] * sc) * (f * omf);
-                    ov[1][j] = d * omf * (sc * fmaf(cp[j], omc, 1.0f));
-                    dh[j] = d * f;
-                }
-                *reinterpret_cast<__nv_bfloat162*>(df_pre + at) = __floats2bfloat162_rn(ov[0][0], ov[0][1]);
-                *reinterpret_cast<__nv_bfloat162*>(dc_pre + at) = __floats2bfloat162_rn(ov[1][0], ov[1][1]);
-                *reinterpret_cast<__nv_bfloat162*>(dg_pre + at) = __floats2bfloat162_rn(ov[2][0], ov[2][1]);
-            }
+            if (i >= n) continue;
+            const int64_t o = at + static_cast<int64_t>(i) * p.D;
+            const f2 d = f2_add(dg[i], dh);
+            *reinterpret_cast<uint32_t*>(p.df_pre + o) = f2_to_bf16(f2_mul(d, xf[i]));
+            *reinterpret_cast<uint32_t*>(p.dc_pre + o) = f2_to_bf16(f2_mul(d, xc[i]));
+            dh = f2_mul(d, fg[i]);
         }
     }
-    if (dh0) *reinterpret_cast<float2*>(dh0 + b * D + k) = make_float2(dh[0], dh[1]);
+    if (p.dh0 && it.seg == 0) *reinterpret_cast<float2*>(p.dh0 + it.b * p.D + it.k) = f2_get(dh);
 }
 
 }  // namespace mmf
