@@ -117,6 +117,8 @@ mmf_status device_state(DeviceState** out) {
         if (e == cudaSuccess) e = set_smem(gemm_bwd_kernel<0>, BwLayout<0>::smem_bytes);
         if (e == cudaSuccess) e = set_smem(gemm_bwd_kernel<1>, BwLayout<1>::smem_bytes);
         if (e == cudaSuccess) e = set_smem(mlgru_scan_tma_kernel, kStSmemBytes);
+        if (e == cudaSuccess) e = set_smem(mlgru_scan_bwd_maps_tma_kernel, kSbMapsSmem);
+        if (e == cudaSuccess) e = set_smem(mlgru_scan_bwd_tma_kernel, kSbBwdSmem);
         if (e != cudaSuccess) return MMF_ERR_CUDA;
         // how many clusters of k CTAs of the decode tensor-core kernel (one CTA
         // per SM) the GPU holds at once: its plan keeps a launch to one wave
@@ -651,6 +653,19 @@ ScanBwdPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D) {
     pl.subs_per_seg = static_cast<int>(std::min<int64_t>(per, pl.subs));
     pl.segments = (pl.subs + pl.subs_per_seg - 1) / pl.subs_per_seg;
     return pl;
+}
+
+// A [B][T][D] bf16 tensor in copies of kSbSub tokens x 64 channels.
+mmf_status encode_scan(CUtensorMap* map, const void* base, int64_t B, int64_t T, int64_t D) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(B)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * D), static_cast<cuuint64_t>(2 * T * D)};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(kSbSub), 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    if (g_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return MMF_ERR_CUDA;
+    return MMF_OK;
 }
 
 struct ScanBwdWorkspace {
@@ -1218,6 +1233,17 @@ int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre, const uint1
     p.subs_per_seg = pl.subs_per_seg;
     p.tiles = pl.tiles;
     p.items = B * pl.segments * static_cast<int64_t>(pl.tiles);
+    if (D % 8 == 0 && D >= 64 && T >= kSbSub && 2 * T * D < (int64_t(1) << 40)) {
+        ScanBwdMaps maps;
+        const std::pair<CUtensorMap*, const void*> all[7] = {{&maps.f, f_pre},   {&maps.c, c_pre},   {&maps.g, g_pre},
+                                                             {&maps.d_o, d_o},   {&maps.df, df_pre}, {&maps.dc, dc_pre},
+                                                             {&maps.dg, dg_pre}};
+        for (const auto& m : all)
+            if ((st = encode_scan(m.first, m.second, B, T, D)) != MMF_OK) return st;
+        const dim3 grid(static_cast<unsigned>((p.items + kSbtWarps - 1) / kSbtWarps)), block(kSbtWarps * 32);
+        if ((st = launch(mlgru_scan_bwd_maps_tma_kernel, grid, block, kSbMapsSmem, s, false, p, maps)) != MMF_OK) return st;
+        return launch(mlgru_scan_bwd_tma_kernel, grid, block, kSbBwdSmem, s, true, p, maps);
+    }
     const dim3 grid(static_cast<unsigned>((p.items + kSbWarps - 1) / kSbWarps)), block(kSbWarps * 32);
     if ((st = launch(mlgru_scan_bwd_maps_kernel, grid, block, 0, s, false, p)) != MMF_OK) return st;
     return launch(mlgru_scan_bwd_kernel, grid, block, 0, s, true, p);
