@@ -87,6 +87,13 @@ cudaError_t set_gemv_attrs() {
     return e;
 }
 
+template <int GW>
+cudaError_t set_scan_bwd_attrs() {
+    cudaError_t e = set_smem(mlgru_scan_bwd_maps_tma_kernel<GW>, sb_smem(GW));
+    if (e == cudaSuccess) e = set_smem(mlgru_scan_bwd_tma_kernel<GW>, sb_smem(GW));
+    return e;
+}
+
 // Per-device one-time set-up (device properties, kernel attributes, the driver
 // entry point for tensor maps).  Must run before any stream capture.
 mmf_status device_state(DeviceState** out) {
@@ -117,8 +124,10 @@ mmf_status device_state(DeviceState** out) {
         if (e == cudaSuccess) e = set_smem(gemm_bwd_kernel<0>, BwLayout<0>::smem_bytes);
         if (e == cudaSuccess) e = set_smem(gemm_bwd_kernel<1>, BwLayout<1>::smem_bytes);
         if (e == cudaSuccess) e = set_smem(mlgru_scan_tma_kernel, kStSmemBytes);
-        if (e == cudaSuccess) e = set_smem(mlgru_scan_bwd_maps_tma_kernel, kSbMapsSmem);
-        if (e == cudaSuccess) e = set_smem(mlgru_scan_bwd_tma_kernel, kSbBwdSmem);
+        if (e == cudaSuccess) e = set_scan_bwd_attrs<1>();
+        if (e == cudaSuccess) e = set_scan_bwd_attrs<2>();
+        if (e == cudaSuccess) e = set_scan_bwd_attrs<3>();
+        if (e == cudaSuccess) e = set_scan_bwd_attrs<4>();
         if (e != cudaSuccess) return MMF_ERR_CUDA;
         // how many clusters of k CTAs of the decode tensor-core kernel (one CTA
         // per SM) the GPU holds at once: its plan keeps a launch to one wave
@@ -634,38 +643,62 @@ mmf_status check_scan_shape(int64_t B, int64_t T, int64_t D) {
     return MMF_OK;
 }
 
-// How the recurrence's gradient splits a sequence: segments of whole
-// kSbSub-token steps, as many as give the GPU kSbItems warps to run, but of at
-// least kSbMinTokens tokens, since each folds the maps of all others.
-constexpr int64_t kSbItems = 148 * 32;
-constexpr int64_t kSbMinTokens = 64;
-
+// How the recurrence's gradient splits its work: CTAs (of gw warps with tensor
+// copies, else of single warps) over channel groups, sequences and segments of
+// whole kSbSub-token steps.  Segments are as many as keep the time of all waves
+// of resident CTAs shortest, a CTA's time being its steps, about two steps to
+// begin and end, and 0.15 steps for each other segment whose map it folds.
 struct ScanBwdPlan {
-    int tiles, subs, subs_per_seg, segments;
+    bool tma;
+    int gw, groups, subs, subs_per_seg, segments;
 };
 
 ScanBwdPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D) {
     ScanBwdPlan pl;
-    pl.tiles = static_cast<int>((D + 63) / 64);
+    pl.tma = D % 8 == 0 && D >= 64 && T >= kSbSub && 2 * T * D < (int64_t(1) << 40);
+    const int64_t tiles = (D + 63) / 64;
+    pl.gw = 1;
+    if (pl.tma)  // the widest CTA that wastes no more than a quarter of its channels
+        for (int gw = 2; gw <= kSbMaxGw; ++gw)
+            if (4 * ((tiles + gw - 1) / gw * gw) <= 5 * tiles) pl.gw = gw;
+    pl.groups = static_cast<int>((tiles + pl.gw - 1) / pl.gw);
     pl.subs = static_cast<int>((T + kSbSub - 1) / kSbSub);
-    const int64_t want = (kSbItems + B * pl.tiles - 1) / (B * pl.tiles);
-    const int64_t per = std::max((pl.subs + want - 1) / want, kSbMinTokens / kSbSub);
-    pl.subs_per_seg = static_cast<int>(std::min<int64_t>(per, pl.subs));
-    pl.segments = (pl.subs + pl.subs_per_seg - 1) / pl.subs_per_seg;
+    const int64_t slots = int64_t(148) * 16 / pl.gw, units = B * pl.groups;
+    double best = 0.0;
+    for (int waves = 1; waves <= 4; ++waves) {
+        const int64_t s = std::max<int64_t>(1, std::min<int64_t>(waves * slots / units, pl.subs));
+        const int per = static_cast<int>((pl.subs + s - 1) / s);
+        const int segments = (pl.subs + per - 1) / per;
+        const int64_t rounds = (units * segments + slots - 1) / slots;
+        const double cost = static_cast<double>(rounds) * (per + 2.0 + 0.15 * segments);
+        if (waves == 1 || cost < best) {
+            best = cost;
+            pl.subs_per_seg = per;
+            pl.segments = segments;
+        }
+    }
     return pl;
 }
 
-// A [B][T][D] bf16 tensor in copies of kSbSub tokens x 64 channels.
-mmf_status encode_scan(CUtensorMap* map, const void* base, int64_t B, int64_t T, int64_t D) {
+// A [B][T][D] bf16 tensor in copies of kSbSub tokens x 64 gw channels.
+mmf_status encode_scan(CUtensorMap* map, const void* base, int64_t B, int64_t T, int64_t D, int gw) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(B)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * D), static_cast<cuuint64_t>(2 * T * D)};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(kSbSub), 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(64 * gw), static_cast<cuuint32_t>(kSbSub), 1};
     const cuuint32_t es[3] = {1, 1, 1};
     if (g_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return MMF_ERR_CUDA;
     return MMF_OK;
+}
+
+template <int GW>
+mmf_status launch_scan_bwd(const ScanBwdParams& p, const ScanBwdMaps& maps, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(p.items)), block(GW * 32);
+    const mmf_status st = launch(mlgru_scan_bwd_maps_tma_kernel<GW>, grid, block, sb_smem(GW), s, false, p, maps);
+    if (st != MMF_OK) return st;
+    return launch(mlgru_scan_bwd_tma_kernel<GW>, grid, block, sb_smem(GW), s, true, p, maps);
 }
 
 struct ScanBwdWorkspace {
@@ -1231,18 +1264,21 @@ int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre, const uint1
     p.S = pl.segments;
     p.subs = pl.subs;
     p.subs_per_seg = pl.subs_per_seg;
-    p.tiles = pl.tiles;
-    p.items = B * pl.segments * static_cast<int64_t>(pl.tiles);
-    if (D % 8 == 0 && D >= 64 && T >= kSbSub && 2 * T * D < (int64_t(1) << 40)) {
+    p.tiles = pl.groups;
+    p.items = B * pl.segments * static_cast<int64_t>(pl.groups);
+    if (pl.tma) {
         ScanBwdMaps maps;
         const std::pair<CUtensorMap*, const void*> all[7] = {{&maps.f, f_pre},   {&maps.c, c_pre},   {&maps.g, g_pre},
                                                              {&maps.d_o, d_o},   {&maps.df, df_pre}, {&maps.dc, dc_pre},
                                                              {&maps.dg, dg_pre}};
         for (const auto& m : all)
-            if ((st = encode_scan(m.first, m.second, B, T, D)) != MMF_OK) return st;
-        const dim3 grid(static_cast<unsigned>((p.items + kSbtWarps - 1) / kSbtWarps)), block(kSbtWarps * 32);
-        if ((st = launch(mlgru_scan_bwd_maps_tma_kernel, grid, block, kSbMapsSmem, s, false, p, maps)) != MMF_OK) return st;
-        return launch(mlgru_scan_bwd_tma_kernel, grid, block, kSbBwdSmem, s, true, p, maps);
+            if ((st = encode_scan(m.first, m.second, B, T, D, pl.gw)) != MMF_OK) return st;
+        switch (pl.gw) {
+            case 1: return launch_scan_bwd<1>(p, maps, s);
+            case 2: return launch_scan_bwd<2>(p, maps, s);
+            case 3: return launch_scan_bwd<3>(p, maps, s);
+            default: return launch_scan_bwd<4>(p, maps, s);
+        }
     }
     const dim3 grid(static_cast<unsigned>((p.items + kSbWarps - 1) / kSbWarps)), block(kSbWarps * 32);
     if ((st = launch(mlgru_scan_bwd_maps_kernel, grid, block, 0, s, false, p)) != MMF_OK) return st;

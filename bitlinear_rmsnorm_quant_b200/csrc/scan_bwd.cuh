@@ -246,22 +246,22 @@ __global__ void __launch_bounds__(kSbWarps * 32, 4) mlgru_scan_bwd_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
-// The same two kernels with the tensors moved by tensor copies: every warp has
-// a ring of kSbStages stages in shared memory, a stage holding kSbSub tokens x
-// 64 channels of f, c, g and do; its first lane keeps the copies kSbStages
-// ahead of the computation, and the gradients leave through two staging
-// buffers by tensor copies too.  The maps are [B][T][D] bf16, so a copy stops
-// at the sequence's end (what it reads beyond is zeros, what it would write
-// beyond is dropped).  Needs D % 8 == 0 (16-byte row pitch), D >= 64 and
-// T >= kSbSub; other shapes take the kernels above.
+// The same two kernels with the tensors moved by tensor copies.  A CTA of GW
+// warps takes GW * 64 neighbouring channels of one segment, a warp 64 of them;
+// kSbSub tokens of f, c, g and do at a time come into a ring of kSbStages
+// stages in shared memory; a lane leaves df, dc and dg where it read f, c and g,
+// and they are copied out from there.  After the one barrier per kSbSub tokens
+// the first thread starts the copies out of this stage and, once those of the
+// stage before have been read, the copies in for the stage after the next.  The maps are [B][T][D] bf16, so a copy stops at the sequence's end
+// (what it reads beyond is zeros, what it would write beyond is dropped).
+// Needs D % 8 == 0 (16-byte row pitch), D >= 64 and T >= kSbSub; other shapes
+// take the kernels above.
 // ---------------------------------------------------------------------------
-constexpr int kSbtWarps = 8;
-constexpr int kSbStages = 2;
-constexpr uint32_t kSbTile = kSbSub * 64 * 2;       // one tensor's tokens of a stage: 1 KB
-constexpr uint32_t kSbStage = 4 * kSbTile;          // f, c, g, do
-constexpr uint32_t kSbOut = 3 * kSbTile;            // df, dc, dg
-constexpr size_t kSbMapsSmem = size_t(kSbtWarps) * kSbStages * kSbStage;
-constexpr size_t kSbBwdSmem = size_t(kSbtWarps) * (kSbStages * kSbStage + 2 * kSbOut);
+constexpr int kSbStages = 3;
+constexpr int kSbMaxGw = 4;
+__host__ __device__ constexpr uint32_t sb_tile(int gw) { return kSbSub * 128u * gw; }  // one tensor's kSbSub tokens
+__host__ __device__ constexpr uint32_t sb_stage(int gw) { return 4 * sb_tile(gw); }    // f, c, g, do
+__host__ __device__ constexpr size_t sb_smem(int gw) { return kSbStages * size_t(sb_stage(gw)); }
 
 struct ScanBwdMaps {
     CUtensorMap f, c, g, d_o, df, dc, dg;
@@ -289,180 +289,184 @@ __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
-// A warp's ring: stage i (of its own count) holds sub-chunk first + i * step.
-struct ScanRing {
-    const ScanBwdMaps* maps;
-    uint8_t* tiles;
-    uint64_t* full;
-    int x, z, first, step, count;
-
-    __device__ __forceinline__ void issue(int i) const {  // by one lane
-        const int slot = i % kSbStages;
-        uint8_t* dst = tiles + slot * kSbStage;
-        const int y = (first + i * step) * kSbSub;
-        mbar_arrive_expect_tx(&full[slot], kSbStage);
-        tma_load_3d(dst, &maps->f, x, y, z, &full[slot]);
-        tma_load_3d(dst + kSbTile, &maps->c, x, y, z, &full[slot]);
-        tma_load_3d(dst + 2 * kSbTile, &maps->g, x, y, z, &full[slot]);
-        tma_load_3d(dst + 3 * kSbTile, &maps->d_o, x, y, z, &full[slot]);
-    }
-    __device__ __forceinline__ void start(int lane) const {
-        if (lane == 0) {
-            for (int i = 0; i < kSbStages; ++i) mbar_init(&full[i], 1);
-            mbar_fence_init();
-            for (int i = 0; i < kSbStages && i < count; ++i) issue(i);
-        }
-        __syncwarp();
-    }
-    // stage i has landed; when the wait gives up, the copies still in flight are
-    // waited for (bounded too) and the warp leaves
-    __device__ __forceinline__ bool wait(int i, volatile int* abort_flag) const {
-        const bool ok = mbar_wait(&full[i % kSbStages], (i / kSbStages) & 1, abort_flag);
-        if (__all_sync(0xffffffffu, ok)) return true;
-        for (int j = i; j < i + kSbStages && j < count; ++j) {
-            const unsigned long long t0 = globaltimer_ns();
-            while (!mbar_try_wait(&full[j % kSbStages], (j / kSbStages) & 1) && globaltimer_ns() - t0 <= kWaitLimitNs) {
-            }
-        }
-        return false;
-    }
-    // every lane has read stage i: its slot takes the stage kSbStages on
-    __device__ __forceinline__ void release(int i, int lane) const {
-        __syncwarp();
-        if (lane == 0 && i + kSbStages < count) issue(i + kSbStages);
+// The CTA's place: its sequence, segment and first channel.
+struct ScanPlace {
+    int b, seg, x, sub0, sub1;
+    __device__ __forceinline__ ScanPlace(const ScanBwdParams& p, unsigned item, int gw) {
+        const unsigned groups = static_cast<unsigned>(p.tiles);
+        const unsigned bs = item / groups;
+        x = static_cast<int>(item - bs * groups) * 64 * gw;
+        b = static_cast<int>(bs / static_cast<unsigned>(p.S));
+        seg = static_cast<int>(bs - static_cast<unsigned>(b) * static_cast<unsigned>(p.S));
+        sub0 = seg * p.subs_per_seg;
+        sub1 = min(p.subs, sub0 + p.subs_per_seg);
     }
 };
 
-__device__ __forceinline__ uint32_t tile_pair(const uint8_t* stage, int tensor, int i, int lane) {
-    return *reinterpret_cast<const uint32_t*>(stage + tensor * kSbTile + i * 128 + 4 * lane);
+template <int GW>
+__device__ __forceinline__ void scan_stage_load(const ScanBwdMaps& maps, uint8_t* dst, uint64_t* full, int x, int sub, int b) {
+    mbar_arrive_expect_tx(full, sb_stage(GW));
+    tma_load_3d(dst, &maps.f, x, sub * kSbSub, b, full);
+    tma_load_3d(dst + sb_tile(GW), &maps.c, x, sub * kSbSub, b, full);
+    tma_load_3d(dst + 2 * sb_tile(GW), &maps.g, x, sub * kSbSub, b, full);
+    tma_load_3d(dst + 3 * sb_tile(GW), &maps.d_o, x, sub * kSbSub, b, full);
 }
 
-__global__ void __launch_bounds__(kSbtWarps * 32) mlgru_scan_bwd_maps_tma_kernel(const ScanBwdParams p,
-                                                                                const __grid_constant__ ScanBwdMaps maps) {
+// Waits for stage j of the CTA's ring.  A thread whose wait gives up (and sets
+// the abort flag, so every other's does) waits for the copies still in flight,
+// bounded too, and leaves; a barrier does not count threads that have left.
+template <int IN_FLIGHT>
+__device__ __forceinline__ bool scan_stage_wait(uint64_t* full, int j, int count, volatile int* abort_flag) {
+    if (mbar_wait(&full[j % kSbStages], (j / kSbStages) & 1, abort_flag)) return true;
+    for (int i = j; i < j + IN_FLIGHT && i < count; ++i) {
+        const unsigned long long t0 = globaltimer_ns();
+        while (!mbar_try_wait(&full[i % kSbStages], (i / kSbStages) & 1) && globaltimer_ns() - t0 <= kWaitLimitNs) {
+        }
+    }
+    return false;
+}
+
+template <int GW>
+__device__ __forceinline__ uint32_t tile_pair(const uint8_t* mine, int tensor, int i) {
+    return *reinterpret_cast<const uint32_t*>(mine + tensor * sb_tile(GW) + i * (128 * GW));
+}
+
+template <int GW>
+__global__ void __launch_bounds__(GW * 32) mlgru_scan_bwd_maps_tma_kernel(const ScanBwdParams p,
+                                                                         const __grid_constant__ ScanBwdMaps maps) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t full[kSbtWarps * kSbStages];
+    __shared__ uint64_t full[kSbStages];
     __shared__ int abort_flag;
     pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) abort_flag = 0;
+    const ScanPlace at(p, blockIdx.x, GW);
+    const int count = at.sub1 - at.sub0;
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < kSbStages; ++i) mbar_init(&full[i], 1);
+        mbar_fence_init();
+        for (int i = 0; i < kSbStages && i < count; ++i)
+            scan_stage_load<GW>(maps, smem + i * sb_stage(GW), &full[i], at.x, at.sub0 + i, at.b);
+    }
     __syncthreads();
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kSbtWarps + warp;
-    if (item >= p.items) return;
-    const ScanItem it(p, item);
-    const int sub0 = it.seg * p.subs_per_seg, sub1 = min(p.subs, sub0 + p.subs_per_seg);
+    const int k = at.x + 2 * static_cast<int>(threadIdx.x);  // this lane's channels k, k + 1
+    const bool valid = k < p.D;                              // D is even, so k + 1 < D too
     const int64_t half = p.D / 2;
-    const ScanRing ring{&maps, smem + size_t(warp) * kSbStages * kSbStage, full + warp * kSbStages,
-                        it.k - 2 * lane, static_cast<int>(it.b), sub0, 1, sub1 - sub0};
-    ring.start(lane);
     f2 A = f2_set(1.0f), P = f2_set(0.0f), R = f2_set(0.0f);
-    float4* part = p.part + (it.b * p.subs + sub0) * half + it.k / 2;
-    for (int j = 0; j < ring.count; ++j) {
-        if (it.valid) {
+    float4* part = p.part + (static_cast<int64_t>(at.b) * p.subs + at.sub0) * half + k / 2;
+    for (int j = 0; j < count; ++j) {
+        if (valid) {
             const float2 a = f2_get(A), q = f2_get(P);
             *part = make_float4(a.x, a.y, q.x, q.y);
         }
         part += half;
-        if (!ring.wait(j, &abort_flag)) return;
-        const uint8_t* st = ring.tiles + (j % kSbStages) * kSbStage;
-        const auto token = [&](int i) {
-            const ScanGates t(tile_pair(st, 0, i, lane), tile_pair(st, 1, i, lane), tile_pair(st, 2, i, lane));
-            A = f2_mul(A, t.f);
-            P = f2_fma(t.f, P, f2_mul(f2_mul(t.ef, t.f), f2_mul(t.cp, t.s)));
-            R = f2_fma(A, f2_mul(f2_bf16(tile_pair(st, 3, i, lane)), t.g), R);
-        };
-        const int n = p.T - (sub0 + j) * kSbSub;
-        if (n >= kSbSub) {
+        if (!scan_stage_wait<kSbStages>(full, j, count, &abort_flag)) return;  // the others find the abort flag set
+        const uint8_t* mine = smem + (j % kSbStages) * sb_stage(GW) + 4 * threadIdx.x;
+        // the gates of kBatch tokens side by side (their chains of dependent
+        // instructions overlap), then their turns in the recurrences
+        constexpr int kBatch = 4;
+        const int n = p.T - (at.sub0 + j) * kSbSub;
 #pragma unroll
-            for (int i = 0; i < kSbSub; ++i) token(i);
-        } else {
-            for (int i = 0; i < n; ++i) token(i);
+        for (int i0 = 0; i0 < kSbSub; i0 += kBatch) {
+            f2 f[kBatch], q[kBatch], x[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const ScanGates t(tile_pair<GW>(mine, 0, i0 + i), tile_pair<GW>(mine, 1, i0 + i),
+                                  tile_pair<GW>(mine, 2, i0 + i));
+                f[i] = t.f;
+                q[i] = f2_mul(f2_mul(t.ef, t.f), f2_mul(t.cp, t.s));
+                x[i] = f2_mul(f2_bf16(tile_pair<GW>(mine, 3, i0 + i)), t.g);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (i0 + i >= n) break;
+                A = f2_mul(A, f[i]);
+                P = f2_fma(f[i], P, q[i]);
+                R = f2_fma(A, x[i], R);
+            }
         }
-        ring.release(j, lane);
+        __syncthreads();  // the stage has been read
+        if (threadIdx.x == 0 && j + kSbStages < count)
+            scan_stage_load<GW>(maps, smem + (j % kSbStages) * sb_stage(GW), &full[j % kSbStages], at.x,
+                                at.sub0 + j + kSbStages, at.b);
     }
-    if (!it.valid) return;
+    if (!valid) return;
     const float2 a = f2_get(A), q = f2_get(P), r = f2_get(R);
-    const int64_t to = (it.b * p.S + it.seg) * half + it.k / 2;
+    const int64_t to = (static_cast<int64_t>(at.b) * p.S + at.seg) * half + k / 2;
     p.seg[to] = make_float4(a.x, a.y, q.x, q.y);
     p.seg_r[to] = r;
 }
 
-__global__ void __launch_bounds__(kSbtWarps * 32, 2) mlgru_scan_bwd_tma_kernel(const ScanBwdParams p,
+template <int GW>
+__global__ void __launch_bounds__(GW * 32, 16 / GW) mlgru_scan_bwd_tma_kernel(const ScanBwdParams p,
                                                                              const __grid_constant__ ScanBwdMaps maps) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t full[kSbtWarps * kSbStages];
+    __shared__ uint64_t full[kSbStages];
     __shared__ int abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) abort_flag = 0;
-    __syncthreads();
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kSbtWarps + warp;
-    if (item >= p.items) return;
     // the last segments first: the maps kernel has just read them
-    const ScanItem it(p, p.items - 1 - item);
-    const int sub0 = it.seg * p.subs_per_seg, sub1 = min(p.subs, sub0 + p.subs_per_seg);
+    const ScanPlace at(p, gridDim.x - 1 - blockIdx.x, GW);
+    const int count = at.sub1 - at.sub0;
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < kSbStages; ++i) mbar_init(&full[i], 1);
+        mbar_fence_init();
+        for (int i = 0; i < kSbStages - 1 && i < count; ++i)
+            scan_stage_load<GW>(maps, smem + i * sb_stage(GW), &full[i], at.x, at.sub1 - 1 - i, at.b);
+    }
+    __syncthreads();
+    const int k = at.x + 2 * static_cast<int>(threadIdx.x);
+    const bool valid = k < p.D;
     const int64_t half = p.D / 2;
-    uint8_t* mine = smem + size_t(warp) * (kSbStages * kSbStage + 2 * kSbOut);
-    const ScanRing ring{&maps, mine, full + warp * kSbStages, it.k - 2 * lane, static_cast<int>(it.b), sub1 - 1, -1,
-                        sub1 - sub0};
-    uint8_t* out = mine + kSbStages * kSbStage;
-    ring.start(lane);
     f2 h = f2_set(0.0f), dh = f2_set(0.0f);
-    if (p.h0 && it.valid) h = *reinterpret_cast<const f2*>(p.h0 + it.b * p.D + it.k);
-    if (p.dh_last && it.valid) dh = *reinterpret_cast<const f2*>(p.dh_last + it.b * p.D + it.k);
+    if (p.h0 && valid) h = *reinterpret_cast<const f2*>(p.h0 + static_cast<int64_t>(at.b) * p.D + k);
+    if (p.dh_last && valid) dh = *reinterpret_cast<const f2*>(p.dh_last + static_cast<int64_t>(at.b) * p.D + k);
     pdl_wait();
-    if (it.valid) {
-        const float4* seg = p.seg + it.b * p.S * half + it.k / 2;
-        const float2* seg_r = p.seg_r + it.b * p.S * half + it.k / 2;
-#pragma unroll 4
-        for (int s = 0; s < it.seg; ++s) {
+    if (valid) {
+        const float4* seg = p.seg + static_cast<int64_t>(at.b) * p.S * half + k / 2;
+        const float2* seg_r = p.seg_r + static_cast<int64_t>(at.b) * p.S * half + k / 2;
+#pragma unroll 8
+        for (int s = 0; s < at.seg; ++s) {
             const float4 m = seg[s * half];
             h = f2_fma(f2_make(m.x, m.y), h, f2_make(m.z, m.w));
         }
-#pragma unroll 4
-        for (int s = p.S - 1; s > it.seg; --s) {
+#pragma unroll 8
+        for (int s = p.S - 1; s > at.seg; --s) {
             const float4 m = seg[s * half];
             const float2 r = seg_r[s * half];
             dh = f2_fma(f2_make(m.x, m.y), dh, f2_make(r.x, r.y));
         }
     }
-    const float4* part = p.part + (it.b * p.subs + sub1 - 1) * half + it.k / 2;
-    float4 next = it.valid ? *part : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int j = 0; j < ring.count; ++j) {
-        const int sub = sub1 - 1 - j;
+    const float4* part = p.part + (static_cast<int64_t>(at.b) * p.subs + at.sub1 - 1) * half + k / 2;
+    float4 next = valid ? *part : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j = 0; j < count; ++j) {
+        const int sub = at.sub1 - 1 - j;
         const float4 m = next;
-        if (it.valid && j + 1 < ring.count) next = *(part -= half);
+        if (valid && j + 1 < count) next = *(part -= half);
         f2 hs = f2_fma(f2_make(m.x, m.y), h, f2_make(m.z, m.w));  // the state before these tokens
-        if (!ring.wait(j, &abort_flag)) {
-            bulk_wait_read<0>();
-            return;
-        }
-        const uint8_t* st = ring.tiles + (j % kSbStages) * kSbStage;
-        uint8_t* to = out + (j & 1) * kSbOut + 4 * lane;
-        if (lane == 0) bulk_wait_read<1>();  // the staging buffer of two steps ago has been read
-        __syncwarp();
+        if (!scan_stage_wait<kSbStages - 1>(full, j, count, &abort_flag)) break;  // the others find the abort flag set
+        uint8_t* mine = smem + (j % kSbStages) * sb_stage(GW) + 4 * threadIdx.x;
         // of each token: what dh is multiplied with for df_pre, dc_pre and the token before, and do g
         f2 xf[kSbSub], xc[kSbSub], fg[kSbSub], dg[kSbSub];
         const auto ahead = [&](int i) {
-            const ScanGates t(tile_pair(st, 0, i, lane), tile_pair(st, 1, i, lane), tile_pair(st, 2, i, lane));
+            const ScanGates t(tile_pair<GW>(mine, 0, i), tile_pair<GW>(mine, 1, i), tile_pair<GW>(mine, 2, i));
             const f2 omf = f2_mul(t.ef, t.f);   // 1 - f
             const f2 c = f2_mul(t.cp, t.s);
             xf[i] = f2_mul(f2_fma(c, f2_set(-1.0f), hs), f2_mul(t.f, omf));
             xc[i] = f2_mul(omf, f2_mul(t.s, f2_fma(t.cp, f2_mul(t.ec, t.s), f2_set(1.0f))));
             hs = f2_fma(t.f, hs, f2_mul(omf, c));
             fg[i] = t.f;
-            dg[i] = f2_mul(f2_bf16(tile_pair(st, 3, i, lane)), t.g);
-            *reinterpret_cast<uint32_t*>(to + 2 * kSbTile + i * 128) =
+            dg[i] = f2_mul(f2_bf16(tile_pair<GW>(mine, 3, i)), t.g);
+            *reinterpret_cast<uint32_t*>(mine + 2 * sb_tile(GW) + i * (128 * GW)) =
                 f2_to_bf16(f2_mul(f2_mul(dg[i], hs), f2_mul(t.eg, t.g)));
         };
         const auto back = [&](int i) {
             const f2 d = f2_add(dg[i], dh);
-            *reinterpret_cast<uint32_t*>(to + i * 128) = f2_to_bf16(f2_mul(d, xf[i]));
-            *reinterpret_cast<uint32_t*>(to + kSbTile + i * 128) = f2_to_bf16(f2_mul(d, xc[i]));
+            *reinterpret_cast<uint32_t*>(mine + i * (128 * GW)) = f2_to_bf16(f2_mul(d, xf[i]));
+            *reinterpret_cast<uint32_t*>(mine + sb_tile(GW) + i * (128 * GW)) = f2_to_bf16(f2_mul(d, xc[i]));
             dh = f2_mul(d, fg[i]);
         };
         const int n = p.T - sub * kSbSub;
 #pragma unroll
         for (int i = 0; i < kSbSub; ++i) ahead(i);  // tokens past the end read zeros and are not written
-        ring.release(j, lane);
         if (n >= kSbSub) {
 #pragma unroll
             for (int i = kSbSub - 1; i >= 0; --i) back(i);
@@ -472,17 +476,24 @@ __global__ void __launch_bounds__(kSbtWarps * 32, 2) mlgru_scan_bwd_tma_kernel(c
                 if (i < n) back(i);
         }
         fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            const uint8_t* from = out + (j & 1) * kSbOut;
-            tma_store_3d(&maps.df, from, ring.x, sub * kSbSub, ring.z);
-            tma_store_3d(&maps.dc, from + kSbTile, ring.x, sub * kSbSub, ring.z);
-            tma_store_3d(&maps.dg, from + 2 * kSbTile, ring.x, sub * kSbSub, ring.z);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            const uint8_t* from = smem + (j % kSbStages) * sb_stage(GW);
+            tma_store_3d(&maps.df, from, at.x, sub * kSbSub, at.b);
+            tma_store_3d(&maps.dc, from + sb_tile(GW), at.x, sub * kSbSub, at.b);
+            tma_store_3d(&maps.dg, from + 2 * sb_tile(GW), at.x, sub * kSbSub, at.b);
             bulk_commit();
+            constexpr int ahead_by = kSbStages - 1;
+            if (j + ahead_by < count) {
+                const int slot = (j + ahead_by) % kSbStages;
+                bulk_wait_read<1>();  // the copies out of this slot, a stage ago, have been read
+                scan_stage_load<GW>(maps, smem + slot * sb_stage(GW), &full[slot], at.x, sub - ahead_by, at.b);
+            }
         }
     }
-    if (lane == 0) bulk_wait_read<0>();
-    if (p.dh0 && it.valid && it.seg == 0) *reinterpret_cast<float2*>(p.dh0 + it.b * p.D + it.k) = f2_get(dh);
+    if (threadIdx.x == 0) bulk_wait_read<0>();
+    if (p.dh0 && valid && at.seg == 0)
+        *reinterpret_cast<float2*>(p.dh0 + static_cast<int64_t>(at.b) * p.D + k) = f2_get(dh);
 }
 
 }  // namespace mmf
