@@ -48,6 +48,31 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const Id* __re
 }
 
 // ---------------------------------------------------------------------------
+// Rows of dtable that no token names.  embed_count_kernel marks the others in
+// used[]; the sorting and summing launches behind it have CTAs of their own
+// that write zeros to a share of the unmarked rows, a warp to a row, so that
+// the writes (most of the work of a small batch and a large table) run beside
+// the sort and the sums.
+// ---------------------------------------------------------------------------
+struct ZeroParams {
+    float* dtable;
+    const uint8_t* used;
+    int begin, end;  // rows of this launch
+    int ctas;        // CTAs of this launch that zero; 0: none
+    int K;
+};
+
+__device__ __forceinline__ void embed_zero(const ZeroParams& z, int cta) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int stride = z.ctas * warps;
+    for (int row = z.begin + cta * warps + warp; row < z.end; row += stride) {
+        if (z.used[row]) continue;
+        float4* to = reinterpret_cast<float4*>(z.dtable + static_cast<int64_t>(row) * z.K);
+        for (int i = lane; i < z.K / 4; i += 32) __stcs(to + i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+    }
+}
+
+// ---------------------------------------------------------------------------
 // The tokens in the order of their ids, equal ids in the order of the tokens:
 // a least-significant-digit radix sort of (id, token) with at most 8 bits a
 // pass.  The places are split over at most kSortCtas CTAs; a CTA counts the
@@ -59,6 +84,7 @@ constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortCtas = 128;
 constexpr int kSortBins = 256;
+constexpr int kSortMaxPasses = 4;   // keys of 31 bits
 
 struct SortParams {
     const void* ids;        // first pass: the caller's ids
@@ -70,7 +96,12 @@ struct SortParams {
     int64_t V;
     int M;
     int per;                // places per CTA, a multiple of kSortThreads
+    int ctas;
     int shift, mask;        // digit = (key >> shift) & mask
+    int* next_count;        // the next pass's counts, taken while placing; null in the last pass
+    int later_counts;       // first pass: how many later passes' counts, one behind another, to zero
+    int next_shift;
+    uint8_t* used;          // first pass, may be null: marks the rows that tokens name
 };
 
 template <typename Id, bool FIRST>
@@ -80,38 +111,45 @@ __device__ __forceinline__ uint32_t sort_key(const SortParams& p, int i) {
     return static_cast<uint32_t>(id < 0 ? p.V : id);
 }
 
-template <typename Id, bool FIRST>
+// The first pass's counts, and zeros for the later ones'.
+template <typename Id>
 __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const SortParams p) {
     __shared__ int bins[kSortBins];
+    pdl_launch_dependents();
     bins[threadIdx.x] = 0;
     __syncthreads();
     const int begin = blockIdx.x * p.per, end = min(p.M, begin + p.per);
-    for (int i = begin + threadIdx.x; i < end; i += kSortThreads)
-        atomicAdd(&bins[(sort_key<Id, FIRST>(p, i) >> p.shift) & p.mask], 1);
+    for (int i = begin + threadIdx.x; i < end; i += kSortThreads) {
+        const uint32_t key = sort_key<Id, true>(p, i);
+        atomicAdd(&bins[(key >> p.shift) & p.mask], 1);
+        if (p.used && key < p.V) p.used[key] = 1;
+    }
     __syncthreads();
     p.count[blockIdx.x * kSortBins + threadIdx.x] = bins[threadIdx.x];
+    for (int i = 0; i < p.later_counts; ++i)
+        p.next_count[(i * kSortCtas + blockIdx.x) * kSortBins + threadIdx.x] = 0;
 }
 
-// The lanes of the warp (among `active`) whose digit is this lane's.
-__device__ __forceinline__ uint32_t sort_peers(uint32_t active, int digit) { return __match_any_sync(active, digit); }
-
 template <typename Id, bool FIRST>
-__global__ void __launch_bounds__(kSortThreads) embed_place_kernel(const SortParams p) {
+__global__ void __launch_bounds__(kSortThreads) embed_place_kernel(const SortParams p, const ZeroParams z) {
     __shared__ int base[kSortBins];                  // where this CTA's next place with a digit goes
     __shared__ int wcount[kSortWarps][kSortBins];    // a round's digits per warp, then the places before each warp's
-    __shared__ int total[kSortBins];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (static_cast<int>(blockIdx.x) >= p.ctas) {
+        embed_zero(z, blockIdx.x - p.ctas);
+        return;
+    }
     {
         // digit t: places of all CTAs, and of the CTAs before this one
         int before = 0, all = 0;
-#pragma unroll 4
-        for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+#pragma unroll 16
+        for (int b = 0; b < p.ctas; ++b) {
             const int c = p.count[b * kSortBins + t];
             all += c;
             if (b < static_cast<int>(blockIdx.x)) before += c;
         }
-        total[t] = all;
-        __syncthreads();
         // exclusive sum of the totals over the digits: 8 warps of 32, then the warps before
         int v = all;
 #pragma unroll
@@ -139,7 +177,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(const SortPar
             key = sort_key<Id, FIRST>(p, i);
             pos = FIRST ? static_cast<uint32_t>(i) : p.pos_in[i];
             digit = static_cast<int>((key >> p.shift) & static_cast<uint32_t>(p.mask));
-            peers = sort_peers(active, digit);
+            peers = __match_any_sync(active, digit);  // the warp's lanes with the same digit
             if ((peers & ((1u << lane) - 1)) == 0) wcount[warp][digit] = __popc(peers);
         }
         __syncthreads();
@@ -155,6 +193,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(const SortPar
             const int to = base[digit] + wcount[warp][digit] + __popc(peers & ((1u << lane) - 1));
             p.key_out[to] = key;
             p.pos_out[to] = pos;
+            if (p.next_count)
+                atomicAdd(&p.next_count[to / p.per * kSortBins + static_cast<int>((key >> p.next_shift) & static_cast<uint32_t>(p.mask))], 1);
         }
         __syncthreads();
         base[t] += sum;
@@ -196,43 +236,69 @@ __device__ __forceinline__ void embed_store8(float* dst, const float (&a)[8], fl
     d[1] = hi;
 }
 
-__global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParams p) {
-    const int begin = blockIdx.x * p.per, end = min(p.M, begin + p.per);
-    const int k = 8 * (blockIdx.y * kEmbedThreads + threadIdx.x);
+constexpr int kSumMaxPer = 256;
+constexpr int kSumBatch = 8;  // rows of dx in flight per thread
+
+__global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParams p, const ZeroParams z) {
+    __shared__ uint32_t key[kSumMaxPer + 1], pos[kSumMaxPer];
+    pdl_launch_dependents();
+    pdl_wait();
+    if (static_cast<int>(blockIdx.x) < z.ctas) {  // these first: they write all the while
+        if (blockIdx.y == 0) embed_zero(z, blockIdx.x);
+        return;
+    }
+    const int cta = blockIdx.x - z.ctas;
+    const int begin = cta * p.per, n = min(p.M - begin, p.per);
+    for (int i = threadIdx.x; i <= n; i += blockDim.x) {
+        key[i] = begin + i < p.M ? p.key[begin + i] : 0xffffffffu;
+        if (i < n) pos[i] = p.pos[begin + i];
+    }
+    const bool began_before = begin > 0 && p.key[begin - 1] == p.key[begin];
+    __syncthreads();
+    const int k = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
     if (k >= p.K) return;
     float a[8] = {};
-    uint32_t run = p.key[begin];
-    bool from_before = begin > 0 && p.key[begin - 1] == run;
-    for (int i = begin; i < end; ++i) {
-        if (run >= p.V) return;  // the places without a row come last
-        float v[8];
-        unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.dx + static_cast<int64_t>(p.pos[i]) * p.K + k)), v);
+    bool from_before = began_before;
+    for (int i0 = 0; i0 < n; i0 += kSumBatch) {
+        uint4 row[kSumBatch];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] += v[j];
-        const uint32_t next = i + 1 < p.M ? p.key[i + 1] : 0xffffffffu;
-        if (next == run && i + 1 < end) continue;
-        if (from_before || next == run) {
-            float* to = (from_before ? p.head : p.tail) + static_cast<int64_t>(blockIdx.x) * p.K + k;
-            reinterpret_cast<float4*>(to)[0] = make_float4(a[0], a[1], a[2], a[3]);
-            reinterpret_cast<float4*>(to)[1] = make_float4(a[4], a[5], a[6], a[7]);
-        } else {
-            embed_store8(p.dtable + static_cast<int64_t>(run) * p.K + k, a, p.scale, p.accumulate);
+        for (int u = 0; u < kSumBatch; ++u)
+            if (i0 + u < n && key[i0 + u] < p.V)
+                row[u] = __ldcs(reinterpret_cast<const uint4*>(p.dx + static_cast<int64_t>(pos[i0 + u]) * p.K + k));
+#pragma unroll
+        for (int u = 0; u < kSumBatch; ++u) {
+            const int i = i0 + u;
+            if (i >= n) break;
+            const uint32_t run = key[i], next = key[i + 1];
+            if (run >= p.V) return;  // the places without a row come last
+            float v[8];
+            unpack_bf16x8(row[u], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] += v[j];
+            if (next == run && i + 1 < n) continue;
+            if (from_before || next == run) {
+                float* to = (from_before ? p.head : p.tail) + static_cast<int64_t>(cta) * p.K + k;
+                reinterpret_cast<float4*>(to)[0] = make_float4(a[0], a[1], a[2], a[3]);
+                reinterpret_cast<float4*>(to)[1] = make_float4(a[4], a[5], a[6], a[7]);
+            } else {
+                embed_store8(p.dtable + static_cast<int64_t>(run) * p.K + k, a, p.scale, p.accumulate);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] = 0.0f;
+            from_before = false;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = 0.0f;
-        from_before = false;
-        run = next;
     }
 }
 
 // CTA b joins the run that begins among its places and goes on behind them.
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const SumParams p) {
+    pdl_wait();
     const int begin = blockIdx.x * p.per, end = min(p.M, begin + p.per);
     if (end >= p.M) return;
     const uint32_t run = p.key[end - 1];
     if (run >= p.V || p.key[end] != run) return;                              // it ends here
     if (p.key[begin] == run && begin > 0 && p.key[begin - 1] == run) return;  // it began earlier
-    const int k = 8 * (blockIdx.y * kEmbedThreads + threadIdx.x);
+    const int k = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
     if (k >= p.K) return;
     double a[8];
     const float* part = p.tail + static_cast<int64_t>(blockIdx.x) * p.K + k;
@@ -251,6 +317,71 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const SumPara
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] = static_cast<float>(a[j]);
     embed_store8(p.dtable + static_cast<int64_t>(run) * p.K + k, s, p.scale, p.accumulate);
+}
+
+// ---------------------------------------------------------------------------
+// A few tokens: one launch, nothing sorted.  A CTA per token (and 8 columns
+// per thread) reads all ids; the first token of an id lists the others in
+// order and adds their rows, in fp32 up to 64 at a time and those in fp64; the
+// CTAs of the later ones leave at once.
+// ---------------------------------------------------------------------------
+constexpr int kFewTokens = 1024;
+constexpr int kFewGroup = 64;
+
+template <typename Id>
+__global__ void __launch_bounds__(kEmbedThreads) embed_few_kernel(const Id* __restrict__ ids,
+                                                                 const uint16_t* __restrict__ dx, int64_t V, int M,
+                                                                 int K, float scale, float* __restrict__ dtable,
+                                                                 int accumulate) {
+    __shared__ int key[kFewTokens];
+    __shared__ int pos[kFewTokens];
+    __shared__ int count;
+    const int m = blockIdx.x;
+    for (int i = threadIdx.x; i < M; i += blockDim.x) key[i] = static_cast<int>(embed_id(ids, i, V));
+    __syncthreads();
+    const int mine = key[m];
+    bool later = mine < 0;
+    for (int i = threadIdx.x; i < m; i += blockDim.x) later |= key[i] == mine;
+    if (__syncthreads_or(later)) return;
+    if (threadIdx.x < 32) {
+        int n = 0;
+        for (int i0 = m; i0 < M; i0 += 32) {
+            const int i = i0 + static_cast<int>(threadIdx.x);
+            const bool same = i < M && key[i] == mine;
+            const uint32_t who = __ballot_sync(0xffffffffu, same);
+            if (same) pos[n + __popc(who & ((1u << threadIdx.x) - 1))] = i;
+            n += __popc(who);
+        }
+        if (threadIdx.x == 0) count = n;
+    }
+    __syncthreads();
+    const int k = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
+    if (k >= K) return;
+    double total[8] = {};
+    for (int g = 0; g < count; g += kFewGroup) {
+        const int end = min(count, g + kFewGroup);
+        float a[8] = {};
+        for (int i0 = g; i0 < end; i0 += kSumBatch) {
+            uint4 row[kSumBatch];
+#pragma unroll
+            for (int u = 0; u < kSumBatch; ++u)
+                if (i0 + u < end) row[u] = __ldg(reinterpret_cast<const uint4*>(dx + static_cast<int64_t>(pos[i0 + u]) * K + k));
+#pragma unroll
+            for (int u = 0; u < kSumBatch; ++u) {
+                if (i0 + u >= end) break;
+                float v[8];
+                unpack_bf16x8(row[u], v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a[j] += v[j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) total[j] += a[j];
+    }
+    float s[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = static_cast<float>(total[j]);
+    embed_store8(dtable + static_cast<int64_t>(mine) * K + k, s, scale, accumulate);
 }
 
 }  // namespace mmf

@@ -557,20 +557,26 @@ mmf_status check_embed_shape(int64_t V, int64_t M, int64_t K) {
 }
 
 // How the embedding gradient splits M places: over the sorting CTAs (a
-// multiple of kSortThreads each) and over the summing CTAs.
+// multiple of kSortThreads each) and over the summing CTAs; and its columns.
 struct EmbedPlan {
+    bool few;
     int sort_per, sort_ctas;
     int sum_per, sum_ctas;
     int passes, digit_bits;
+    int threads, col_tiles;  // 8 columns per thread
 };
 
-EmbedPlan embed_plan(int64_t V, int64_t M) {
+EmbedPlan embed_plan(int64_t V, int64_t M, int64_t K) {
     EmbedPlan pl{};
-    if (M == 0) return pl;
+    const int lanes = static_cast<int>(K / 8);
+    pl.col_tiles = (lanes + kEmbedThreads - 1) / kEmbedThreads;
+    pl.threads = ((lanes + pl.col_tiles - 1) / pl.col_tiles + 31) / 32 * 32;
+    pl.few = M <= kFewTokens;
+    if (pl.few) return pl;
     const int64_t per = (M + kSortCtas - 1) / kSortCtas;
     pl.sort_per = static_cast<int>((per + kSortThreads - 1) / kSortThreads * kSortThreads);
     pl.sort_ctas = static_cast<int>((M + pl.sort_per - 1) / pl.sort_per);
-    pl.sum_per = M <= 131072 ? 64 : 256;
+    pl.sum_per = M <= 32768 ? 32 : M <= (1 << 20) ? 64 : kSumMaxPer;
     pl.sum_ctas = static_cast<int>((M + pl.sum_per - 1) / pl.sum_per);
     int bits = 0;  // of the keys 0 .. V
     while ((V >> bits) != 0) ++bits;
@@ -582,13 +588,14 @@ EmbedPlan embed_plan(int64_t V, int64_t M) {
 struct EmbedWorkspace {
     uint32_t* key[2];
     uint32_t* pos[2];
-    int* count;
+    int* count[kSortMaxPasses];  // one behind another
+    uint8_t* used;
     float* head;
     float* tail;
     size_t bytes;
 };
 
-EmbedWorkspace carve_embed(void* ws, const EmbedPlan& pl, int64_t M, int64_t K) {
+EmbedWorkspace carve_embed(void* ws, const EmbedPlan& pl, int64_t V, int64_t M, int64_t K) {
     uint8_t* b = static_cast<uint8_t*>(ws);
     size_t at = 0;
     const auto take = [&](size_t bytes) {
@@ -596,12 +603,15 @@ EmbedWorkspace carve_embed(void* ws, const EmbedPlan& pl, int64_t M, int64_t K) 
         at += align256(bytes);
         return r;
     };
-    EmbedWorkspace w;
+    EmbedWorkspace w{};
+    if (pl.few) return w;
     for (int i = 0; i < 2; ++i) {
         w.key[i] = reinterpret_cast<uint32_t*>(take(4 * static_cast<size_t>(M)));
         w.pos[i] = reinterpret_cast<uint32_t*>(take(4 * static_cast<size_t>(M)));
     }
-    w.count = reinterpret_cast<int*>(take(sizeof(int) * kSortCtas * kSortBins));
+    for (int i = 0; i < kSortMaxPasses; ++i)
+        w.count[i] = reinterpret_cast<int*>(take(sizeof(int) * kSortCtas * kSortBins));
+    w.used = take(static_cast<size_t>(V));
     const size_t parts = 4 * static_cast<size_t>(pl.sum_ctas) * static_cast<size_t>(K);
     w.head = reinterpret_cast<float*>(take(parts));
     w.tail = reinterpret_cast<float*>(take(parts));
@@ -609,9 +619,13 @@ EmbedWorkspace carve_embed(void* ws, const EmbedPlan& pl, int64_t M, int64_t K) 
     return w;
 }
 
+// Sorts the places by id; the placing launches also zero shares of the rows
+// that no token names, as much as they write while the sort runs, and z is
+// left with the rest.
 template <typename Id>
 mmf_status embed_sort(const void* ids, int64_t V, int64_t M, const EmbedPlan& pl, const EmbedWorkspace& w,
-                      cudaStream_t s) {
+                      ZeroParams* z, int num_sms, cudaStream_t s) {
+    constexpr int64_t kShareBytes = int64_t(16) << 20;
     for (int i = 0; i < pl.passes; ++i) {
         SortParams p{};
         p.ids = ids;
@@ -619,18 +633,29 @@ mmf_status embed_sort(const void* ids, int64_t V, int64_t M, const EmbedPlan& pl
         p.pos_in = w.pos[(i + 1) & 1];
         p.key_out = w.key[i & 1];
         p.pos_out = w.pos[i & 1];
-        p.count = w.count;
+        p.count = w.count[i];
         p.V = V;
         p.M = static_cast<int>(M);
         p.per = pl.sort_per;
+        p.ctas = pl.sort_ctas;
         p.shift = i * pl.digit_bits;
         p.mask = (1 << pl.digit_bits) - 1;
-        const dim3 grid(static_cast<unsigned>(pl.sort_ctas)), block(kSortThreads);
-        mmf_status st = i == 0 ? launch(embed_count_kernel<Id, true>, grid, block, 0, s, false, p)
-                               : launch(embed_count_kernel<Id, false>, grid, block, 0, s, false, p);
-        if (st != MMF_OK) return st;
-        st = i == 0 ? launch(embed_place_kernel<Id, true>, grid, block, 0, s, false, p)
-                    : launch(embed_place_kernel<Id, false>, grid, block, 0, s, false, p);
+        p.next_count = i + 1 < pl.passes ? w.count[i + 1] : nullptr;
+        p.later_counts = pl.passes - 1;
+        p.next_shift = p.shift + pl.digit_bits;
+        p.used = z->ctas > 0 ? w.used : nullptr;
+        const dim3 block(kSortThreads);
+        mmf_status st;
+        if (i == 0 &&
+            (st = launch(embed_count_kernel<Id>, dim3(static_cast<unsigned>(pl.sort_ctas)), block, 0, s, false, p)) != MMF_OK)
+            return st;
+        ZeroParams share = *z;
+        share.end = static_cast<int>(std::min<int64_t>(z->end, z->begin + kShareBytes / (4 * z->K)));
+        share.ctas = share.end > share.begin ? num_sms : 0;
+        z->begin = share.end;
+        const dim3 grid(static_cast<unsigned>(pl.sort_ctas + share.ctas));
+        st = i == 0 ? launch(embed_place_kernel<Id, true>, grid, block, 0, s, true, p, share)
+                    : launch(embed_place_kernel<Id, false>, grid, block, 0, s, true, p, share);
         if (st != MMF_OK) return st;
     }
     return MMF_OK;
@@ -1171,8 +1196,8 @@ int mmf_embed_fwd(const void* ids, const void* table, float scale, int64_t V, in
 }
 
 size_t mmf_embed_bwd_workspace_bytes(int64_t V, int64_t M, int64_t K) {
-    if (check_embed_shape(V, M, K) != MMF_OK || V == 0 || M == 0) return 0;
-    return carve_embed(nullptr, embed_plan(V, M), M, K).bytes;
+    if (check_embed_shape(V, M, K) != MMF_OK || V == 0) return 0;
+    return carve_embed(nullptr, embed_plan(V, M, K), V, M, K).bytes;
 }
 
 int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, int64_t M, int64_t K, float* dtable,
@@ -1180,21 +1205,42 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, i
     if (!std::isfinite(scale) || (flags & ~(MMF_EMBED_IDS64 | MMF_EMBED_ACCUMULATE)) != 0) return MMF_ERR_INVALID_ARG;
     mmf_status st = check_embed_shape(V, M, K);
     if (st != MMF_OK) return st;
-    const bool accumulate = (flags & MMF_EMBED_ACCUMULATE) != 0;
+    const bool accumulate = (flags & MMF_EMBED_ACCUMULATE) != 0, wide = (flags & MMF_EMBED_IDS64) != 0;
     if (V == 0 || (M == 0 && accumulate)) return MMF_OK;
     if (!dtable || (M > 0 && (!ids || !dx))) return MMF_ERR_INVALID_ARG;
     if (!aligned16(ids) || !aligned16(dx) || !aligned16(dtable) || !aligned16(workspace)) return MMF_ERR_MISALIGNED;
-    const EmbedPlan pl = embed_plan(V, M);
-    const EmbedWorkspace w = carve_embed(workspace, pl, M, K);
-    if (M > 0 && (!workspace || workspace_bytes < w.bytes)) return MMF_ERR_WORKSPACE;
+    const EmbedPlan pl = embed_plan(V, M, K);
+    const EmbedWorkspace w = carve_embed(workspace, pl, V, M, K);
+    if (w.bytes > 0 && (!workspace || workspace_bytes < w.bytes)) return MMF_ERR_WORKSPACE;
     DeviceState* dev;
     if ((st = device_state(&dev)) != MMF_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!accumulate && cudaMemsetAsync(dtable, 0, 4 * static_cast<size_t>(V) * static_cast<size_t>(K), s) != cudaSuccess)
-        return MMF_ERR_CUDA;
-    if (M == 0) return MMF_OK;
-    st = (flags & MMF_EMBED_IDS64) ? embed_sort<int64_t>(ids, V, M, pl, w, s) : embed_sort<int32_t>(ids, V, M, pl, w, s);
+    const dim3 block(static_cast<unsigned>(pl.threads));
+    if (pl.few) {
+        if (!accumulate &&
+            cudaMemsetAsync(dtable, 0, 4 * static_cast<size_t>(V) * static_cast<size_t>(K), s) != cudaSuccess)
+            return MMF_ERR_CUDA;
+        if (M == 0) return MMF_OK;
+        const dim3 grid(static_cast<unsigned>(M), static_cast<unsigned>(pl.col_tiles));
+        const int m = static_cast<int>(M), k = static_cast<int>(K), add = accumulate;
+        return wide ? launch(embed_few_kernel<int64_t>, grid, block, 0, s, false, static_cast<const int64_t*>(ids), dx,
+                             V, m, k, scale, dtable, add)
+                    : launch(embed_few_kernel<int32_t>, grid, block, 0, s, false, static_cast<const int32_t*>(ids), dx,
+                             V, m, k, scale, dtable, add);
+    }
+    ZeroParams z{};
+    z.dtable = dtable;
+    z.used = w.used;
+    z.K = static_cast<int>(K);
+    if (!accumulate) {
+        z.end = static_cast<int>(V);
+        z.ctas = 2 * dev->num_sms;
+        if (cudaMemsetAsync(w.used, 0, static_cast<size_t>(V), s) != cudaSuccess) return MMF_ERR_CUDA;
+    }
+    st = wide ? embed_sort<int64_t>(ids, V, M, pl, w, &z, dev->num_sms, s)
+              : embed_sort<int32_t>(ids, V, M, pl, w, &z, dev->num_sms, s);
     if (st != MMF_OK) return st;
+    if (z.begin >= z.end) z.ctas = 0;
     SumParams p{};
     p.key = w.key[(pl.passes - 1) & 1];
     p.pos = w.pos[(pl.passes - 1) & 1];
@@ -1208,10 +1254,11 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, i
     p.per = pl.sum_per;
     p.scale = scale;
     p.accumulate = accumulate;
-    const dim3 grid(static_cast<unsigned>(pl.sum_ctas),
-                    static_cast<unsigned>((K + 8 * kEmbedThreads - 1) / (8 * kEmbedThreads)));
-    if ((st = launch(embed_sum_kernel, grid, dim3(kEmbedThreads), 0, s, false, p)) != MMF_OK) return st;
-    return launch(embed_join_kernel, grid, dim3(kEmbedThreads), 0, s, false, p);
+    const unsigned tiles = static_cast<unsigned>(pl.col_tiles);
+    if ((st = launch(embed_sum_kernel, dim3(static_cast<unsigned>(z.ctas + pl.sum_ctas), tiles), block, 0, s, true, p,
+                     z)) != MMF_OK)
+        return st;
+    return launch(embed_join_kernel, dim3(static_cast<unsigned>(pl.sum_ctas), tiles), block, 0, s, true, p);
 }
 
 size_t mmf_mlgru_scan_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D) {

@@ -90,6 +90,8 @@ class MMFError(RuntimeError):
 def lib() -> C.CDLL:
     """Loads libmmf.so (once); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -293,26 +295,31 @@ def bitlinear_fwd_noalloc(x: torch.Tensor, gamma: torch.Tensor, packed: torch.Te
     return y
 
 
-def _on(device: torch.device, stream, call):
-    """call(stream handle) with the tensors' device current and, when a stream is given, with it as torch's
-    current stream, so that what the call allocates belongs to the stream that uses it."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
-    with torch.cuda.device(device):
+# The current stream's handle of a device by its index.  torch.cuda.current_stream builds a Stream object first
+# (3.3 us a call on the host, as long as a kernel's launch; this takes 0.1 us).
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on(index: int, stream, call):
+    """call(stream handle) with the tensors' device (its index) current and, when a stream is given, with it as
+    torch's current stream, so that what the call allocates belongs to the stream that uses it."""
+    if stream is None and index == torch.cuda.current_device():
+        return call(_current_raw_stream(index))
+    with torch.cuda.device(index):
         if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(_current_raw_stream(index))
         s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
         with torch.cuda.stream(s):
             return call(s.cuda_stream)
 
 
-def _like(t: torch.Tensor, dtype, shape, device, name: str):
-    """As _dev, for an argument of a known shape on a known device."""
-    _dev(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _like(t: torch.Tensor, dtype, shape, index: int, name: str):
+    """As _dev, for an argument of a known shape on the CUDA device of a known index."""
+    if t.dtype != dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        _dev(t, dtype, name)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
 def _embed_ids(ids: torch.Tensor) -> int:
@@ -326,22 +333,24 @@ def embed_fwd(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out=No
     """int32/int64 ids[...] and fp32/bf16 table[V, K] -> bf16 x[..., K] = scale * table[ids]; an id outside
     [0, V) gives a row of zeros."""
     flags = _embed_ids(ids)
-    if table.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"table must be torch.float32 or torch.bfloat16, got {table.dtype}")
-    _like(table, table.dtype, table.shape, ids.device, "table")
+    index = ids.get_device()
     if table.dtype == torch.bfloat16:
         flags |= EMBED_TABLE_BF16
+    elif table.dtype != torch.float32:
+        raise TypeError(f"table must be torch.float32 or torch.bfloat16, got {table.dtype}")
     V, K = table.shape
+    _like(table, table.dtype, (V, K), index, "table")
+    shape = (*ids.shape, K)
     if out is not None:
-        _like(out, torch.bfloat16, (*ids.shape, K), ids.device, "out")
+        _like(out, torch.bfloat16, shape, index, "out")
 
     def call(s):
-        x = out if out is not None else torch.empty((*ids.shape, K), dtype=torch.bfloat16, device=ids.device)
+        x = out if out is not None else torch.empty(shape, dtype=torch.bfloat16, device=ids.device)
         check(lib().mmf_embed_fwd(ids.data_ptr(), table.data_ptr(), scale, V, ids.numel(), K, x.data_ptr(), flags, s),
               "mmf_embed_fwd")
         return x
 
-    return _on(ids.device, stream, call)
+    return _on(index, stream, call)
 
 
 def embed_bwd_workspace_bytes(V: int, M: int, K: int) -> int:
@@ -353,10 +362,11 @@ def embed_bwd(ids: torch.Tensor, dx: torch.Tensor, V: int, scale: float = 1.0, o
     """Gradient of embed_fwd for its table: int32/int64 ids[...] and bf16 dx[..., K] -> fp32 dtable[V, K];
     with accumulate the sums are added to `out`, and rows no id names stay as they are."""
     flags = _embed_ids(ids)
+    index = ids.get_device()
     K = dx.shape[-1]
-    _like(dx, torch.bfloat16, (*ids.shape, K), ids.device, "dx")
+    _like(dx, torch.bfloat16, (*ids.shape, K), index, "dx")
     if out is not None:
-        _like(out, torch.float32, (V, K), ids.device, "out")
+        _like(out, torch.float32, (V, K), index, "out")
     if accumulate:
         if out is None:
             raise ValueError("accumulate adds to out: out is missing")
@@ -364,18 +374,21 @@ def embed_bwd(ids: torch.Tensor, dx: torch.Tensor, V: int, scale: float = 1.0, o
     M = ids.numel()
     need = embed_bwd_workspace_bytes(V, M, K)
     if workspace is not None:
-        _like(workspace, torch.uint8, workspace.shape, ids.device, "workspace")
+        _like(workspace, torch.uint8, workspace.shape, index, "workspace")
         if workspace.numel() < need:
             raise ValueError(f"workspace needs {need} bytes")
 
     def call(s):
         d = out if out is not None else torch.empty((V, K), dtype=torch.float32, device=ids.device)
-        ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=ids.device)
-        check(lib().mmf_embed_bwd(ids.data_ptr(), dx.data_ptr(), scale, V, M, K, d.data_ptr(), ws.data_ptr(),
-                                  ws.numel(), flags, s), "mmf_embed_bwd")
+        ws = workspace
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=ids.device)
+        check(lib().mmf_embed_bwd(ids.data_ptr(), dx.data_ptr(), scale, V, M, K, d.data_ptr(),
+                                  ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+                                  flags, s), "mmf_embed_bwd")
         return d
 
-    return _on(ids.device, stream, call)
+    return _on(index, stream, call)
 
 
 def mlgru_scan_bwd_workspace_bytes(B: int, T: int, D: int) -> int:
@@ -388,16 +401,18 @@ def mlgru_scan_bwd(f_pre: torch.Tensor, c_pre: torch.Tensor, g_pre: torch.Tensor
     """Gradient of mlgru_scan: its bf16 [B, T, D] inputs and d_o, the gradient of o (and fp32 [B, D] h0 and
     dh_last) -> (bf16 df_pre, dc_pre, dg_pre [B, T, D], fp32 dh0 [B, D])."""
     _dev(f_pre, torch.bfloat16, "f_pre")
-    B, T, D = f_pre.shape
-    dev = f_pre.device
-    for name, t in (("c_pre", c_pre), ("g_pre", g_pre), ("d_o", d_o)):
-        _like(t, torch.bfloat16, f_pre.shape, dev, name)
+    shape = f_pre.shape
+    B, T, D = shape
+    dev = f_pre.get_device()
+    _like(c_pre, torch.bfloat16, shape, dev, "c_pre")
+    _like(g_pre, torch.bfloat16, shape, dev, "g_pre")
+    _like(d_o, torch.bfloat16, shape, dev, "d_o")
     for name, t in (("h0", h0), ("dh_last", dh_last), ("dh0", dh0)):
         if t is not None:
             _like(t, torch.float32, (B, D), dev, name)
     if outs is not None:
         for name, t in zip(("df_pre", "dc_pre", "dg_pre"), outs, strict=True):
-            _like(t, torch.bfloat16, f_pre.shape, dev, name)
+            _like(t, torch.bfloat16, shape, dev, name)
     need = mlgru_scan_bwd_workspace_bytes(B, T, D)
     if workspace is not None:
         _like(workspace, torch.uint8, workspace.shape, dev, "workspace")
@@ -405,13 +420,18 @@ def mlgru_scan_bwd(f_pre: torch.Tensor, c_pre: torch.Tensor, g_pre: torch.Tensor
             raise ValueError(f"workspace needs {need} bytes")
 
     def call(s):
-        df, dc, dg = outs if outs is not None else [torch.empty_like(f_pre) for _ in range(3)]
-        dh = dh0 if dh0 is not None else torch.empty((B, D), dtype=torch.float32, device=dev)
-        ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=dev)
+        df, dc, dg = outs if outs is not None else (torch.empty_like(f_pre), torch.empty_like(f_pre),
+                                                    torch.empty_like(f_pre))
+        dh = dh0 if dh0 is not None else torch.empty((B, D), dtype=torch.float32, device=f_pre.device)
+        ws = workspace
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=f_pre.device)
         check(lib().mmf_mlgru_scan_bwd(f_pre.data_ptr(), c_pre.data_ptr(), g_pre.data_ptr(), d_o.data_ptr(),
                                        h0.data_ptr() if h0 is not None else None,
                                        dh_last.data_ptr() if dh_last is not None else None, B, T, D, df.data_ptr(),
-                                       dc.data_ptr(), dg.data_ptr(), dh.data_ptr(), ws.data_ptr(), ws.numel(), s),
+                                       dc.data_ptr(), dg.data_ptr(), dh.data_ptr(),
+                                       ws.data_ptr() if ws is not None else None,
+                                       ws.numel() if ws is not None else 0, s),
               "mmf_mlgru_scan_bwd")
         return df, dc, dg, dh
 
@@ -448,7 +468,7 @@ def adamw_state(p: torch.Tensor, bits: int = 32) -> dict:
 _ADAMW_DESC = struct.Struct("<7QqfI")   # mmf_adamw_tensor
 
 
-def _adamw_describe(t: AdamWTensor, device, buf, at: int) -> None:
+def _adamw_describe(t: AdamWTensor, index: int, buf, at: int) -> None:
     p, g, m, v, ms, vs, pb = t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.p_bf16
     n = p.numel()
     flags = 0
@@ -456,29 +476,32 @@ def _adamw_describe(t: AdamWTensor, device, buf, at: int) -> None:
         flags = ADAMW_GRAD_BF16
     elif g.dtype != torch.float32:
         raise TypeError(f"g must be torch.float32 or torch.bfloat16, got {g.dtype}")
+    if p.dtype != torch.float32:
+        raise TypeError(f"p must be torch.float32, got {p.dtype}")
+    msp = vsp = 0
     if m.dtype == torch.float8_e4m3fn:
         flags |= ADAMW_STATE8
         if v.dtype != torch.float8_e5m2:
             raise TypeError(f"v must be torch.float8_e5m2 beside an 8-bit m, got {v.dtype}")
-        blocks = -(-n // ADAMW_BLOCK)
-        for name, s in (("m_scale", ms), ("v_scale", vs)):
-            if s is None:
-                raise ValueError(f"{name} is missing: 8-bit moments need their scales")
-            _like(s, torch.float32, (blocks,), device, name)
+        if ms is None or vs is None:
+            raise ValueError("m_scale and v_scale are missing: 8-bit moments need them")
+        blocks = (-(-n // ADAMW_BLOCK),)
+        _like(ms, torch.float32, blocks, index, "m_scale")
+        _like(vs, torch.float32, blocks, index, "v_scale")
+        msp, vsp = ms.data_ptr(), vs.data_ptr()
     elif m.dtype != torch.float32 or v.dtype != torch.float32 or ms is not None or vs is not None:
         raise TypeError("m and v must be torch.float32, or torch.float8_e4m3fn and torch.float8_e5m2 with their scales")
-    if p.dtype != torch.float32:
-        raise TypeError(f"p must be torch.float32, got {p.dtype}")
+    pbp = 0
     if pb is not None:
-        _like(pb, torch.bfloat16, p.shape, device, "p_bf16")
-    for name, x in (("p", p), ("g", g), ("m", m), ("v", v)):
-        if x.device != device:
-            raise ValueError(f"{name} must be on {device}, got {x.device}")
-        if x.numel() != n or not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous, with as many elements as p")
-    _ADAMW_DESC.pack_into(buf, at, p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(),
-                          ms.data_ptr() if ms is not None else 0, vs.data_ptr() if vs is not None else 0,
-                          pb.data_ptr() if pb is not None else 0, n, t.weight_decay, flags)
+        _like(pb, torch.bfloat16, p.shape, index, "p_bf16")
+        pbp = pb.data_ptr()
+    if not (p.get_device() == g.get_device() == m.get_device() == v.get_device() == index):
+        raise ValueError(f"p, g, m and v must be on cuda:{index}, got {p.device}, {g.device}, {m.device}, {v.device}")
+    if not (g.numel() == m.numel() == v.numel() == n and p.is_contiguous() and g.is_contiguous()
+            and m.is_contiguous() and v.is_contiguous()):
+        raise ValueError("p, g, m and v must be contiguous, with as many elements each")
+    _ADAMW_DESC.pack_into(buf, at, p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), msp, vsp, pbp, n,
+                          t.weight_decay, flags)
 
 
 def _adamw_hyper(step, lr, beta1, beta2, eps, grad_scale, seed) -> AdamWHyper:
@@ -502,14 +525,15 @@ def adamw_step(tensors, step: int, lr: float, beta1: float = 0.9, beta2: float =
     tensors = list(tensors)
     if not tensors:
         return
-    device = tensors[0].p.device
-    if device.type != "cuda":
+    index = tensors[0].p.get_device()
+    if index < 0:
         raise ValueError("p must be a CUDA tensor")
-    buf = bytearray(_ADAMW_DESC.size * len(tensors))
+    size = _ADAMW_DESC.size
+    buf = bytearray(size * len(tensors))
     for i, t in enumerate(tensors):
-        _adamw_describe(t, device, buf, i * _ADAMW_DESC.size)
+        _adamw_describe(t, index, buf, i * size)
     if scalars is not None:
-        _like(scalars, torch.uint8, (32,), device, "scalars")
+        _like(scalars, torch.uint8, (32,), index, "scalars")
     hyper = _adamw_hyper(step, lr, beta1, beta2, eps, grad_scale, seed)
     desc = (C.c_char * len(buf)).from_buffer(buf)
 
@@ -517,7 +541,7 @@ def adamw_step(tensors, step: int, lr: float, beta1: float = 0.9, beta2: float =
         check(lib().mmf_adamw_step(C.addressof(desc), len(tensors), C.addressof(hyper),
                                    scalars.data_ptr() if scalars is not None else None, s), "mmf_adamw_step")
 
-    _on(device, stream, call)
+    _on(index, stream, call)
 
 
 def hbm_copy(src: torch.Tensor, dst: torch.Tensor, stream=None):

@@ -103,17 +103,17 @@ def test_embed_argument_errors(L):
     assert f(MIS, A, 1.0, 100, 4, 64, A, 0, None) == 3
     assert f(None, None, 1.0, 100, 0, 64, None, 0, None) == 0  # no tokens
     g = L.mmf_embed_bwd
-    need = L.mmf_embed_bwd_workspace_bytes(100, 4, 64)
+    need = L.mmf_embed_bwd_workspace_bytes(100, 2000, 64)
     assert need > 0 and L.mmf_embed_bwd_workspace_bytes(100, 0, 64) == 0
-    assert L.mmf_embed_bwd_workspace_bytes(100, 4, 12) == 0
+    assert L.mmf_embed_bwd_workspace_bytes(100, 2000, 12) == 0
     assert g(A, A, 1.0, 100, 4, 64, A, A, need, 2, None) == 1  # the table's type is the lookup's
     assert g(A, A, float("inf"), 100, 4, 64, A, A, need, 0, None) == 1
     assert g(A, None, 1.0, 100, 4, 64, A, A, need, 0, None) == 1
     assert g(A, A, 1.0, 100, 4, 64, None, A, need, 0, None) == 1
     assert g(A, A, 1.0, 100, 4, 65, A, A, need, 0, None) == 2
     assert g(A, A, 1.0, 100, 4, 64, MIS, A, need, 0, None) == 3
-    assert g(A, A, 1.0, 100, 4, 64, A, A, need - 1, 0, None) == 4
-    assert g(A, A, 1.0, 100, 4, 64, A, None, need, 0, None) == 4
+    assert g(A, A, 1.0, 100, 2000, 64, A, A, need - 1, 0, None) == 4
+    assert g(A, A, 1.0, 100, 2000, 64, A, None, need, 0, None) == 4
     assert g(None, None, 1.0, 100, 0, 64, None, None, 0, 4, None) == 0   # nothing to add
     assert g(None, None, 1.0, 0, 4, 64, None, None, 0, 0, None) == 0     # an empty table
     if not torch.cuda.is_available():

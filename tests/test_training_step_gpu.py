@@ -70,12 +70,14 @@ def test_embed_fwd_int64_ids_beyond_32_bits():
 @pytest.mark.parametrize("M,V,K,kind", [
     (1, 100, 2560, "mixed"), (37, 1000, 8, "mixed"), (300, 50, 1000, "mixed"), (2000, 32000, 264, "mixed"),
     (5, 7, 4104, "mixed"), (64, 10, 64, "outside"), (3, 1, 16, "one"),
+    # the most tokens of one launch, and one more
+    (1024, 100, 72, "mixed"), (1024, 9, 136, "one"), (1025, 100, 72, "mixed"), (1030, 9, 2056, "one"),
     # one word for all tokens: a run over every summing CTA; more than one sorting CTA and round
     (1000, 300, 40, "one"), (9000, 70000, 64, "mixed"), (40000, 3, 16, "mixed"), (140000, 1000, 8, "mixed"),
     (140000, 20, 8, "one"),
     # keys of one digit, of exactly 8 and 16 bits, of three digits
-    (500, 255, 16, "mixed"), (500, 256, 16, "mixed"), (500, 65535, 8, "mixed"), (500, 65536, 8, "mixed"),
-    (700, 1 << 20, 8, "mixed")])
+    (1500, 255, 16, "mixed"), (1500, 256, 16, "mixed"), (1500, 65535, 8, "mixed"), (1500, 65536, 8, "mixed"),
+    (1700, 1 << 20, 8, "mixed"), (2000, 5, 16, "outside"), (1200, (1 << 24) + 5, 8, "mixed")])
 @pytest.mark.parametrize("add", [False, True])
 def test_embed_bwd(M, V, K, kind, add):
     rng = np.random.default_rng(M + K)
