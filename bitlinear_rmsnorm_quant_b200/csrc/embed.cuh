@@ -48,27 +48,42 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const Id* __re
 }
 
 // ---------------------------------------------------------------------------
-// Rows of dtable that no token names.  embed_count_kernel marks the others in
-// used[]; the sorting and summing launches behind it have CTAs of their own
-// that write zeros to a share of the unmarked rows, a warp to a row, so that
-// the writes (most of the work of a small batch and a large table) run beside
-// the sort and the sums.
+// Rows of dtable that no token names.  The first counting launch marks the
+// others in used[]; the launches behind it have CTAs of their own that write
+// zeros to a share of the unmarked rows, so that the writes (most of the work
+// of a small batch and a large table) run beside the sort and the sums.  A
+// warp writes kZeroUnits pieces of a row of at most 2 KB and is done: many
+// short CTAs write 6.4 TB/s, 296 that stay 5.9 TB/s (32000 rows of 2560 fp32,
+// 12% of them marked).
 // ---------------------------------------------------------------------------
+constexpr int kZeroUnits = 2;
+constexpr int kZeroPiece = 128;  // 16-byte stores of a piece
+
 struct ZeroParams {
     float* dtable;
     const uint8_t* used;
     int begin, end;  // rows of this launch
-    int ctas;        // CTAs of this launch that zero; 0: none
     int K;
 };
 
+__host__ __device__ __forceinline__ int64_t embed_zero_ctas(const ZeroParams& z, int threads) {
+    const int64_t pieces = (z.K / 4 + kZeroPiece - 1) / kZeroPiece, warps = threads / 32;
+    return (static_cast<int64_t>(z.end - z.begin) * pieces + warps * kZeroUnits - 1) / (warps * kZeroUnits);
+}
+
 __device__ __forceinline__ void embed_zero(const ZeroParams& z, int cta) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int stride = z.ctas * warps;
-    for (int row = z.begin + cta * warps + warp; row < z.end; row += stride) {
-        if (z.used[row]) continue;
-        float4* to = reinterpret_cast<float4*>(z.dtable + static_cast<int64_t>(row) * z.K);
-        for (int i = lane; i < z.K / 4; i += 32) __stcs(to + i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+    const int per_row = z.K / 4, pieces = (per_row + kZeroPiece - 1) / kZeroPiece;
+    const int64_t first = (static_cast<int64_t>(cta) * warps + warp) * kZeroUnits;
+#pragma unroll
+    for (int u = 0; u < kZeroUnits; ++u) {
+        const int64_t row = z.begin + (first + u) / pieces;
+        const int from = static_cast<int>((first + u) % pieces) * kZeroPiece;
+        if (row >= z.end || z.used[row]) continue;
+        float4* to = reinterpret_cast<float4*>(z.dtable + row * z.K);
+#pragma unroll
+        for (int i = 0; i < kZeroPiece; i += 32)
+            if (from + i + lane < per_row) __stcs(to + from + i + lane, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
     }
 }
 
@@ -77,14 +92,14 @@ __device__ __forceinline__ void embed_zero(const ZeroParams& z, int cta) {
 // a least-significant-digit radix sort of (id, token) with at most 8 bits a
 // pass.  The places are split over at most kSortCtas CTAs; a CTA counts the
 // digits of its places (embed_count_kernel), and places them behind those of
-// the CTAs before it (embed_place_kernel).  Ids outside [0, V) sort as V,
+// the CTAs before it (embed_place_kernel; counting the next pass's digits there
+// with atomics took 16 us more at 131072 tokens than the launch it saved).  Ids outside [0, V) sort as V,
 // behind all rows.
 // ---------------------------------------------------------------------------
-constexpr int kSortThreads = 256;
+constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortCtas = 128;
 constexpr int kSortBins = 256;
-constexpr int kSortMaxPasses = 4;   // keys of 31 bits
 
 struct SortParams {
     const void* ids;        // first pass: the caller's ids
@@ -98,9 +113,6 @@ struct SortParams {
     int per;                // places per CTA, a multiple of kSortThreads
     int ctas;
     int shift, mask;        // digit = (key >> shift) & mask
-    int* next_count;        // the next pass's counts, taken while placing; null in the last pass
-    int later_counts;       // first pass: how many later passes' counts, one behind another, to zero
-    int next_shift;
     uint8_t* used;          // first pass, may be null: marks the rows that tokens name
 };
 
@@ -111,29 +123,40 @@ __device__ __forceinline__ uint32_t sort_key(const SortParams& p, int i) {
     return static_cast<uint32_t>(id < 0 ? p.V : id);
 }
 
-// The first pass's counts, and zeros for the later ones'.
-template <typename Id>
-__global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const SortParams p) {
+template <typename Id, bool FIRST>
+__global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const SortParams p, const ZeroParams z) {
     __shared__ int bins[kSortBins];
     pdl_launch_dependents();
-    bins[threadIdx.x] = 0;
+    pdl_wait();
+    if (static_cast<int>(blockIdx.x) >= p.ctas) {
+        embed_zero(z, blockIdx.x - p.ctas);
+        return;
+    }
+    if (threadIdx.x < kSortBins) bins[threadIdx.x] = 0;
     __syncthreads();
     const int begin = blockIdx.x * p.per, end = min(p.M, begin + p.per);
     for (int i = begin + threadIdx.x; i < end; i += kSortThreads) {
-        const uint32_t key = sort_key<Id, true>(p, i);
+        const uint32_t key = sort_key<Id, FIRST>(p, i);
         atomicAdd(&bins[(key >> p.shift) & p.mask], 1);
-        if (p.used && key < p.V) p.used[key] = 1;
+        if (FIRST && p.used && key < p.V) p.used[key] = 1;
     }
     __syncthreads();
-    p.count[blockIdx.x * kSortBins + threadIdx.x] = bins[threadIdx.x];
-    for (int i = 0; i < p.later_counts; ++i)
-        p.next_count[(i * kSortCtas + blockIdx.x) * kSortBins + threadIdx.x] = 0;
+    if (threadIdx.x < kSortBins) p.count[blockIdx.x * kSortBins + threadIdx.x] = bins[threadIdx.x];
+}
+
+// used[] before the first counting launch marks it
+__global__ void __launch_bounds__(kSortThreads) embed_clear_kernel(uint8_t* used, int64_t bytes) {
+    pdl_launch_dependents();
+    const int64_t i = 16 * (static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x);
+    if (i < bytes) *reinterpret_cast<uint4*>(used + i) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 template <typename Id, bool FIRST>
 __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(const SortParams p, const ZeroParams z) {
     __shared__ int base[kSortBins];                  // where this CTA's next place with a digit goes
     __shared__ int wcount[kSortWarps][kSortBins];    // a round's digits per warp, then the places before each warp's
+    __shared__ int part[2][4][kSortBins];            // a quarter of the CTAs' places: all, and before this one
+    __shared__ int wsum[kSortBins / 32];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     pdl_launch_dependents();
     pdl_wait();
@@ -141,87 +164,114 @@ __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(const SortPar
         embed_zero(z, blockIdx.x - p.ctas);
         return;
     }
+    const int begin = blockIdx.x * p.per, end = min(p.M, begin + p.per);
+    uint32_t key = 0, pos = 0;  // of this thread's place in the coming round
+    if (begin + t < end) {
+        key = sort_key<Id, FIRST>(p, begin + t);
+        pos = FIRST ? static_cast<uint32_t>(begin + t) : p.pos_in[begin + t];
+    }
     {
-        // digit t: places of all CTAs, and of the CTAs before this one
+        // digit d: places of all CTAs, and of the CTAs before this one, by quarters
+        const int d = t & (kSortBins - 1), quarter = t / kSortBins;
+        int count[kSortCtas / 4];
+#pragma unroll
+        for (int i = 0; i < kSortCtas / 4; ++i) {
+            const int b = 4 * i + quarter;
+            count[i] = b < p.ctas ? p.count[b * kSortBins + d] : 0;
+        }
         int before = 0, all = 0;
-#pragma unroll 16
-        for (int b = 0; b < p.ctas; ++b) {
-            const int c = p.count[b * kSortBins + t];
-            all += c;
-            if (b < static_cast<int>(blockIdx.x)) before += c;
+#pragma unroll
+        for (int i = 0; i < kSortCtas / 4; ++i) {
+            all += count[i];
+            if (4 * i + quarter < static_cast<int>(blockIdx.x)) before += count[i];
+        }
+        part[0][quarter][d] = all;
+        part[1][quarter][d] = before;
+    }
+    __syncthreads();
+    int all = 0, before = 0, v = 0;
+    if (t < kSortBins) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            all += part[0][q][t];
+            before += part[1][q][t];
         }
         // exclusive sum of the totals over the digits: 8 warps of 32, then the warps before
-        int v = all;
+        v = all;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xffffffffu, v, o);
             if (lane >= o) v += u;
         }
-        if (lane == 31) wcount[0][warp] = v;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) v += wcount[0][w];
-        base[t] = v - all + before;
-        __syncthreads();
+        if (lane == 31) wsum[warp] = v;
     }
-    const int begin = blockIdx.x * p.per, end = min(p.M, begin + p.per);
+    __syncthreads();
+    if (t < kSortBins) {
+        for (int w = 0; w < warp; ++w) v += wsum[w];
+        base[t] = v - all + before;
+    }
     for (int round = begin; round < end; round += kSortThreads) {
-        const int i = round + t;
-        const bool there = i < end;
-#pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) wcount[w][t] = 0;
+        const bool there = round + t < end;
+        for (int i = t; i < kSortWarps * kSortBins; i += kSortThreads) wcount[0][i] = 0;
         __syncthreads();
         const uint32_t active = __ballot_sync(0xffffffffu, there);
-        uint32_t key = 0, pos = 0, peers = 0;
-        int digit = 0;
+        uint32_t peers = 0;
+        const int digit = static_cast<int>((key >> p.shift) & static_cast<uint32_t>(p.mask));
         if (there) {
-            key = sort_key<Id, FIRST>(p, i);
-            pos = FIRST ? static_cast<uint32_t>(i) : p.pos_in[i];
-            digit = static_cast<int>((key >> p.shift) & static_cast<uint32_t>(p.mask));
             peers = __match_any_sync(active, digit);  // the warp's lanes with the same digit
             if ((peers & ((1u << lane) - 1)) == 0) wcount[warp][digit] = __popc(peers);
         }
         __syncthreads();
         int sum = 0;
+        if (t < kSortBins) {
 #pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int c = wcount[w][t];
-            wcount[w][t] = sum;
-            sum += c;
+            for (int w = 0; w < kSortWarps; ++w) {
+                const int c = wcount[w][t];
+                wcount[w][t] = sum;
+                sum += c;
+            }
         }
         __syncthreads();
         if (there) {
             const int to = base[digit] + wcount[warp][digit] + __popc(peers & ((1u << lane) - 1));
             p.key_out[to] = key;
             p.pos_out[to] = pos;
-            if (p.next_count)
-                atomicAdd(&p.next_count[to / p.per * kSortBins + static_cast<int>((key >> p.next_shift) & static_cast<uint32_t>(p.mask))], 1);
+        }
+        const int i = round + kSortThreads + t;
+        if (i < end) {
+            key = sort_key<Id, FIRST>(p, i);
+            pos = FIRST ? static_cast<uint32_t>(i) : p.pos_in[i];
         }
         __syncthreads();
-        base[t] += sum;
+        if (t < kSortBins) base[t] += sum;
     }
 }
 
 // ---------------------------------------------------------------------------
 // Sums of equal ids.  A CTA takes `per` consecutive places of the sorted order
 // and 8 columns per thread; it adds the rows of dx in order, in fp32, and at
-// the end of a run of equal ids writes the row of dtable.  A run that crosses
-// the CTA's places leaves its part in the workspace (the part up to the CTA's
-// last place in tail[], the part from its first place, when the run began
-// earlier, in head[]), and embed_join_kernel adds the parts in order, in fp64.
-// So the order of additions depends on the ids alone.
+// the end of a run of equal ids writes the row of dtable.  A run of at most
+// `per` places is summed by the CTA it begins in, also behind the CTA's own
+// places (and skipped by the next).  Of a longer one each CTA leaves its part
+// in the workspace (the part up to the CTA's last place in tail[], the part
+// from its first place, where the run began earlier, in head[]), and
+// embed_join_kernel adds the parts in order, in fp64.  So the order of
+// additions depends on the ids alone.
 // ---------------------------------------------------------------------------
 struct SumParams {
     const uint32_t* key;
     const uint32_t* pos;
     const uint16_t* dx;
     float* dtable;
-    float* head;  // [CTA][K]
-    float* tail;  // [CTA][K]
+    float* head;         // [CTA][K]
+    float* tail;         // [CTA][K]
+    uint32_t* crossing;  // [CTA] the long run that begins in the CTA and goes on behind it, or kNoRun
     int64_t V;
-    int M, K, per;
+    int M, K, per, ctas;
     float scale;
     int accumulate;
 };
+constexpr uint32_t kNoRun = 0xffffffffu;
 
 __device__ __forceinline__ void embed_store8(float* dst, const float (&a)[8], float scale, bool accumulate) {
     float4 lo = make_float4(a[0] * scale, a[1] * scale, a[2] * scale, a[3] * scale);
@@ -240,42 +290,72 @@ constexpr int kSumMaxPer = 256;
 constexpr int kSumBatch = 8;  // rows of dx in flight per thread
 
 __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParams p, const ZeroParams z) {
-    __shared__ uint32_t key[kSumMaxPer + 1], pos[kSumMaxPer];
+    __shared__ uint32_t keys[3 * kSumMaxPer + 1];  // of places begin - per .. begin + 2 per
+    __shared__ uint32_t pos[2 * kSumMaxPer];
+    __shared__ int head_start, head_end, tail_start, tail_end;
     pdl_launch_dependents();
     pdl_wait();
-    if (static_cast<int>(blockIdx.x) < z.ctas) {  // these first: they write all the while
-        if (blockIdx.y == 0) embed_zero(z, blockIdx.x);
+    const int cta = blockIdx.x;  // the summing CTAs first: they wait for memory most of their time
+    if (cta >= p.ctas) {
+        if (blockIdx.y == 0) embed_zero(z, cta - p.ctas);
         return;
     }
-    const int cta = blockIdx.x - z.ctas;
-    const int begin = cta * p.per, n = min(p.M - begin, p.per);
-    for (int i = threadIdx.x; i <= n; i += blockDim.x) {
-        key[i] = begin + i < p.M ? p.key[begin + i] : 0xffffffffu;
-        if (i < n) pos[i] = p.pos[begin + i];
+    const int begin = cta * p.per, n = min(p.M - begin, p.per), per = p.per;
+    if (threadIdx.x == 0) {
+        head_start = -per;
+        head_end = 2 * per + 1;
+        tail_start = 0;
+        tail_end = 2 * per + 1;
     }
-    const bool began_before = begin > 0 && p.key[begin - 1] == p.key[begin];
+    for (int i = threadIdx.x; i <= 3 * per; i += blockDim.x) {
+        const int at = begin - per + i;
+        keys[i] = at >= 0 && at < p.M ? p.key[at] : kNoRun;
+        if (i >= per && i < 3 * per && at < p.M) pos[i - per] = p.pos[at];
+    }
     __syncthreads();
+    // The runs over the CTA's first and last place, by places counted from
+    // `begin`: where they begin (looked for as far as `per` places before the
+    // CTA) and end (as far as the places loaded).
+    const uint32_t* key = keys + per;
+    const uint32_t first = key[0], last = key[n - 1];
+    for (int i = static_cast<int>(threadIdx.x) - per; i <= 2 * per; i += blockDim.x) {
+        if (i < 0 && key[i] != first) atomicMax(&head_start, i + 1);
+        if (i >= 0 && key[i] != first) atomicMin(&head_end, i);
+        if (i >= 0 && i < n && key[i] != last) atomicMax(&tail_start, i + 1);
+        if (i >= n && key[i] != last) atomicMin(&tail_end, i);
+    }
+    __syncthreads();
+    // the run over the first place began earlier; it is long if it is more than `per` places
+    const bool before = begin > 0 && head_start < 0;
+    const bool head_long = before && head_end - head_start > per;
+    int i0 = before && !head_long ? head_end : 0;
+    // the run over the last place goes on; one that covers the CTA and began earlier is the head's
+    const bool covers = before && tail_start == 0;
+    const bool goes_on = tail_end > n;
+    const bool tail_long = goes_on && (covers ? head_long : tail_end - tail_start > per);
+    const int end = goes_on && !tail_long && !covers ? tail_end : n;
+    if (threadIdx.x == 0 && blockIdx.y == 0) p.crossing[cta] = tail_long && !covers && last < p.V ? last : kNoRun;
     const int k = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
     if (k >= p.K) return;
     float a[8] = {};
-    bool from_before = began_before;
-    for (int i0 = 0; i0 < n; i0 += kSumBatch) {
+    bool from_before = head_long;
+    for (; i0 < end; i0 += kSumBatch) {
         uint4 row[kSumBatch];
 #pragma unroll
         for (int u = 0; u < kSumBatch; ++u)
-            if (i0 + u < n && key[i0 + u] < p.V)
+            if (i0 + u < end && key[i0 + u] < p.V)
                 row[u] = __ldcs(reinterpret_cast<const uint4*>(p.dx + static_cast<int64_t>(pos[i0 + u]) * p.K + k));
 #pragma unroll
         for (int u = 0; u < kSumBatch; ++u) {
             const int i = i0 + u;
-            if (i >= n) break;
+            if (i >= end) break;
             const uint32_t run = key[i], next = key[i + 1];
             if (run >= p.V) return;  // the places without a row come last
             float v[8];
             unpack_bf16x8(row[u], v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) a[j] += v[j];
-            if (next == run && i + 1 < n) continue;
+            if (next == run && i + 1 < end) continue;
             if (from_before || next == run) {
                 float* to = (from_before ? p.head : p.tail) + static_cast<int64_t>(cta) * p.K + k;
                 reinterpret_cast<float4*>(to)[0] = make_float4(a[0], a[1], a[2], a[3]);
@@ -290,33 +370,49 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParam
     }
 }
 
-// CTA b joins the run that begins among its places and goes on behind them.
+// Joins the parts of the long runs; those of kJoin summing CTAs by one CTA.
+constexpr int kJoin = 2;
+
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const SumParams p) {
+    __shared__ uint32_t crossing[kJoin];
     pdl_wait();
-    const int begin = blockIdx.x * p.per, end = min(p.M, begin + p.per);
-    if (end >= p.M) return;
-    const uint32_t run = p.key[end - 1];
-    if (run >= p.V || p.key[end] != run) return;                              // it ends here
-    if (p.key[begin] == run && begin > 0 && p.key[begin - 1] == run) return;  // it began earlier
-    const int k = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
-    if (k >= p.K) return;
-    double a[8];
-    const float* part = p.tail + static_cast<int64_t>(blockIdx.x) * p.K + k;
-    for (int b = blockIdx.x;;) {
-        const float4 lo = reinterpret_cast<const float4*>(part)[0], hi = reinterpret_cast<const float4*>(part)[1];
-        const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        const bool first = b == static_cast<int>(blockIdx.x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = first ? static_cast<double>(v[j]) : a[j] + v[j];
-        ++b;
-        const int64_t at = static_cast<int64_t>(b) * p.per;
-        if (at >= p.M || p.key[at] != run) break;
-        part = p.head + static_cast<int64_t>(b) * p.K + k;
+    if (threadIdx.x < kJoin) {
+        const int b = blockIdx.x * kJoin + threadIdx.x;
+        crossing[threadIdx.x] = b < p.ctas ? p.crossing[b] : kNoRun;
     }
-    float s[8];
+    __syncthreads();
+    const int k = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
+    for (int c = 0; c < kJoin; ++c) {
+        const uint32_t run = crossing[c];
+        if (run == kNoRun) continue;
+        const int b = blockIdx.x * kJoin + c;
+        // how many CTAs behind this one begin inside the run
+        int parts = 0;
+        for (int more = blockDim.x; more == static_cast<int>(blockDim.x); parts += more) {
+            const int64_t at = (static_cast<int64_t>(b) + 1 + parts + threadIdx.x) * p.per;
+            more = __syncthreads_count(at < p.M && p.key[at] == run);
+        }
+        if (k >= p.K) continue;
+        double a[8];
+        {
+            const float4* tail = reinterpret_cast<const float4*>(p.tail + static_cast<int64_t>(b) * p.K + k);
+            const float4 lo = tail[0], hi = tail[1];
+            a[0] = lo.x, a[1] = lo.y, a[2] = lo.z, a[3] = lo.w;
+            a[4] = hi.x, a[5] = hi.y, a[6] = hi.z, a[7] = hi.w;
+        }
+        const float* head = p.head + (static_cast<int64_t>(b) + 1) * p.K + k;
+#pragma unroll 8
+        for (int i = 0; i < parts; ++i) {
+            const float4* part = reinterpret_cast<const float4*>(head + static_cast<int64_t>(i) * p.K);
+            const float4 lo = part[0], hi = part[1];
+            a[0] += lo.x, a[1] += lo.y, a[2] += lo.z, a[3] += lo.w;
+            a[4] += hi.x, a[5] += hi.y, a[6] += hi.z, a[7] += hi.w;
+        }
+        float s[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = static_cast<float>(a[j]);
-    embed_store8(p.dtable + static_cast<int64_t>(run) * p.K + k, s, p.scale, p.accumulate);
+        for (int j = 0; j < 8; ++j) s[j] = static_cast<float>(a[j]);
+        embed_store8(p.dtable + static_cast<int64_t>(run) * p.K + k, s, p.scale, p.accumulate);
+    }
 }
 
 // ---------------------------------------------------------------------------

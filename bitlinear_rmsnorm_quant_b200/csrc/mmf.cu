@@ -588,10 +588,11 @@ EmbedPlan embed_plan(int64_t V, int64_t M, int64_t K) {
 struct EmbedWorkspace {
     uint32_t* key[2];
     uint32_t* pos[2];
-    int* count[kSortMaxPasses];  // one behind another
+    int* count;
     uint8_t* used;
     float* head;
     float* tail;
+    uint32_t* crossing;
     size_t bytes;
 };
 
@@ -609,22 +610,30 @@ EmbedWorkspace carve_embed(void* ws, const EmbedPlan& pl, int64_t V, int64_t M, 
         w.key[i] = reinterpret_cast<uint32_t*>(take(4 * static_cast<size_t>(M)));
         w.pos[i] = reinterpret_cast<uint32_t*>(take(4 * static_cast<size_t>(M)));
     }
-    for (int i = 0; i < kSortMaxPasses; ++i)
-        w.count[i] = reinterpret_cast<int*>(take(sizeof(int) * kSortCtas * kSortBins));
+    w.count = reinterpret_cast<int*>(take(sizeof(int) * kSortCtas * kSortBins));
     w.used = take(static_cast<size_t>(V));
     const size_t parts = 4 * static_cast<size_t>(pl.sum_ctas) * static_cast<size_t>(K);
     w.head = reinterpret_cast<float*>(take(parts));
     w.tail = reinterpret_cast<float*>(take(parts));
+    w.crossing = reinterpret_cast<uint32_t*>(take(4 * static_cast<size_t>(pl.sum_ctas)));
     w.bytes = at;
     return w;
 }
 
-// Sorts the places by id; the placing launches also zero shares of the rows
-// that no token names, as much as they write while the sort runs, and z is
-// left with the rest.
+// The next `bytes` of the rows to zero, taken off z.
+ZeroParams zero_share(ZeroParams* z, int64_t bytes) {
+    ZeroParams share = *z;
+    share.end = static_cast<int>(std::min<int64_t>(z->end, z->begin + bytes / (4 * z->K)));
+    z->begin = share.end;
+    return share;
+}
+
+// Sorts the places by id; the launches after the first also zero shares of the
+// rows that no token names, about what they write while the sort runs, and z is
+// left with the rest.  `used` is null where nothing is to be zeroed.
 template <typename Id>
 mmf_status embed_sort(const void* ids, int64_t V, int64_t M, const EmbedPlan& pl, const EmbedWorkspace& w,
-                      ZeroParams* z, int num_sms, cudaStream_t s) {
+                      uint8_t* used, ZeroParams* z, cudaStream_t s) {
     constexpr int64_t kShareBytes = int64_t(16) << 20;
     for (int i = 0; i < pl.passes; ++i) {
         SortParams p{};
@@ -633,27 +642,22 @@ mmf_status embed_sort(const void* ids, int64_t V, int64_t M, const EmbedPlan& pl
         p.pos_in = w.pos[(i + 1) & 1];
         p.key_out = w.key[i & 1];
         p.pos_out = w.pos[i & 1];
-        p.count = w.count[i];
+        p.count = w.count;
         p.V = V;
         p.M = static_cast<int>(M);
         p.per = pl.sort_per;
         p.ctas = pl.sort_ctas;
         p.shift = i * pl.digit_bits;
         p.mask = (1 << pl.digit_bits) - 1;
-        p.next_count = i + 1 < pl.passes ? w.count[i + 1] : nullptr;
-        p.later_counts = pl.passes - 1;
-        p.next_shift = p.shift + pl.digit_bits;
-        p.used = z->ctas > 0 ? w.used : nullptr;
+        p.used = used;
         const dim3 block(kSortThreads);
-        mmf_status st;
-        if (i == 0 &&
-            (st = launch(embed_count_kernel<Id>, dim3(static_cast<unsigned>(pl.sort_ctas)), block, 0, s, false, p)) != MMF_OK)
-            return st;
-        ZeroParams share = *z;
-        share.end = static_cast<int>(std::min<int64_t>(z->end, z->begin + kShareBytes / (4 * z->K)));
-        share.ctas = share.end > share.begin ? num_sms : 0;
-        z->begin = share.end;
-        const dim3 grid(static_cast<unsigned>(pl.sort_ctas + share.ctas));
+        ZeroParams share = zero_share(z, i == 0 ? 0 : kShareBytes);
+        dim3 grid(static_cast<unsigned>(pl.sort_ctas + embed_zero_ctas(share, kSortThreads)));
+        mmf_status st = i == 0 ? launch(embed_count_kernel<Id, true>, grid, block, 0, s, used != nullptr, p, share)
+                               : launch(embed_count_kernel<Id, false>, grid, block, 0, s, true, p, share);
+        if (st != MMF_OK) return st;
+        share = zero_share(z, kShareBytes);
+        grid = dim3(static_cast<unsigned>(pl.sort_ctas + embed_zero_ctas(share, kSortThreads)));
         st = i == 0 ? launch(embed_place_kernel<Id, true>, grid, block, 0, s, true, p, share)
                     : launch(embed_place_kernel<Id, false>, grid, block, 0, s, true, p, share);
         if (st != MMF_OK) return st;
@@ -1234,13 +1238,14 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, i
     z.K = static_cast<int>(K);
     if (!accumulate) {
         z.end = static_cast<int>(V);
-        z.ctas = 2 * dev->num_sms;
-        if (cudaMemsetAsync(w.used, 0, static_cast<size_t>(V), s) != cudaSuccess) return MMF_ERR_CUDA;
+        const int64_t per_cta = 16 * kSortThreads;
+        if ((st = launch(embed_clear_kernel, dim3(static_cast<unsigned>((V + per_cta - 1) / per_cta)), dim3(kSortThreads),
+                         0, s, false, w.used, V)) != MMF_OK)
+            return st;
     }
-    st = wide ? embed_sort<int64_t>(ids, V, M, pl, w, &z, dev->num_sms, s)
-              : embed_sort<int32_t>(ids, V, M, pl, w, &z, dev->num_sms, s);
+    uint8_t* used = accumulate ? nullptr : w.used;
+    st = wide ? embed_sort<int64_t>(ids, V, M, pl, w, used, &z, s) : embed_sort<int32_t>(ids, V, M, pl, w, used, &z, s);
     if (st != MMF_OK) return st;
-    if (z.begin >= z.end) z.ctas = 0;
     SumParams p{};
     p.key = w.key[(pl.passes - 1) & 1];
     p.pos = w.pos[(pl.passes - 1) & 1];
@@ -1248,17 +1253,20 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, i
     p.dtable = dtable;
     p.head = w.head;
     p.tail = w.tail;
+    p.crossing = w.crossing;
     p.V = V;
     p.M = static_cast<int>(M);
     p.K = static_cast<int>(K);
     p.per = pl.sum_per;
+    p.ctas = pl.sum_ctas;
     p.scale = scale;
     p.accumulate = accumulate;
     const unsigned tiles = static_cast<unsigned>(pl.col_tiles);
-    if ((st = launch(embed_sum_kernel, dim3(static_cast<unsigned>(z.ctas + pl.sum_ctas), tiles), block, 0, s, true, p,
-                     z)) != MMF_OK)
+    if ((st = launch(embed_sum_kernel, dim3(static_cast<unsigned>(pl.sum_ctas + embed_zero_ctas(z, pl.threads)), tiles),
+                     block, 0, s, true, p, z)) != MMF_OK)
         return st;
-    return launch(embed_join_kernel, dim3(static_cast<unsigned>(pl.sum_ctas), tiles), block, 0, s, true, p);
+    return launch(embed_join_kernel, dim3(static_cast<unsigned>((pl.sum_ctas + kJoin - 1) / kJoin), tiles), block, 0, s,
+                  true, p);
 }
 
 size_t mmf_mlgru_scan_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D) {
