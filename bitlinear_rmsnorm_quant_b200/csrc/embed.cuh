@@ -73,16 +73,17 @@ __host__ __device__ __forceinline__ int64_t embed_zero_ctas(const ZeroParams& z,
 
 __device__ __forceinline__ void embed_zero(const ZeroParams& z, int cta) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int per_row = z.K / 4, pieces = (per_row + kZeroPiece - 1) / kZeroPiece;
-    const int64_t first = (static_cast<int64_t>(cta) * warps + warp) * kZeroUnits;
+    const unsigned per_row = z.K / 4, pieces = (per_row + kZeroPiece - 1) / kZeroPiece;
+    const unsigned first = (static_cast<unsigned>(cta) * warps + warp) * kZeroUnits;  // pieces of a table fit 32 bits
 #pragma unroll
     for (int u = 0; u < kZeroUnits; ++u) {
-        const int64_t row = z.begin + (first + u) / pieces;
-        const int from = static_cast<int>((first + u) % pieces) * kZeroPiece;
+        const unsigned of = (first + u) / pieces;
+        const unsigned from = (first + u - of * pieces) * kZeroPiece;
+        const int64_t row = z.begin + static_cast<int64_t>(of);
         if (row >= z.end || z.used[row]) continue;
         float4* to = reinterpret_cast<float4*>(z.dtable + row * z.K);
 #pragma unroll
-        for (int i = 0; i < kZeroPiece; i += 32)
+        for (unsigned i = 0; i < kZeroPiece; i += 32)
             if (from + i + lane < per_row) __stcs(to + from + i + lane, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
     }
 }
@@ -370,49 +371,49 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParam
     }
 }
 
-// Joins the parts of the long runs; those of kJoin summing CTAs by one CTA.
-constexpr int kJoin = 2;
+// Joins the parts of the long runs, a CTA for each summing CTA that one begins
+// in (the others leave at once).  The parts were written up to a whole summing
+// launch ago and are read from HBM behind its last writes, so only those of the
+// run are: first which of the next kJoinBatch CTAs' first places are in it.
+constexpr int kJoinBatch = 8;
 
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const SumParams p) {
-    __shared__ uint32_t crossing[kJoin];
     pdl_wait();
-    if (threadIdx.x < kJoin) {
-        const int b = blockIdx.x * kJoin + threadIdx.x;
-        crossing[threadIdx.x] = b < p.ctas ? p.crossing[b] : kNoRun;
-    }
-    __syncthreads();
+    const uint32_t run = p.crossing[blockIdx.x];
     const int k = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
-    for (int c = 0; c < kJoin; ++c) {
-        const uint32_t run = crossing[c];
-        if (run == kNoRun) continue;
-        const int b = blockIdx.x * kJoin + c;
-        // how many CTAs behind this one begin inside the run
-        int parts = 0;
-        for (int more = blockDim.x; more == static_cast<int>(blockDim.x); parts += more) {
-            const int64_t at = (static_cast<int64_t>(b) + 1 + parts + threadIdx.x) * p.per;
-            more = __syncthreads_count(at < p.M && p.key[at] == run);
-        }
-        if (k >= p.K) continue;
-        double a[8];
-        {
-            const float4* tail = reinterpret_cast<const float4*>(p.tail + static_cast<int64_t>(b) * p.K + k);
-            const float4 lo = tail[0], hi = tail[1];
-            a[0] = lo.x, a[1] = lo.y, a[2] = lo.z, a[3] = lo.w;
-            a[4] = hi.x, a[5] = hi.y, a[6] = hi.z, a[7] = hi.w;
-        }
-        const float* head = p.head + (static_cast<int64_t>(b) + 1) * p.K + k;
-#pragma unroll 8
-        for (int i = 0; i < parts; ++i) {
-            const float4* part = reinterpret_cast<const float4*>(head + static_cast<int64_t>(i) * p.K);
-            const float4 lo = part[0], hi = part[1];
-            a[0] += lo.x, a[1] += lo.y, a[2] += lo.z, a[3] += lo.w;
-            a[4] += hi.x, a[5] += hi.y, a[6] += hi.z, a[7] += hi.w;
-        }
-        float s[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = static_cast<float>(a[j]);
-        embed_store8(p.dtable + static_cast<int64_t>(run) * p.K + k, s, p.scale, p.accumulate);
+    if (run == kNoRun || k >= p.K) return;
+    double a[8];
+    {
+        const float4* tail = reinterpret_cast<const float4*>(p.tail + static_cast<int64_t>(blockIdx.x) * p.K + k);
+        const float4 lo = tail[0], hi = tail[1];
+        a[0] = lo.x, a[1] = lo.y, a[2] = lo.z, a[3] = lo.w;
+        a[4] = hi.x, a[5] = hi.y, a[6] = hi.z, a[7] = hi.w;
     }
+    int parts = kJoinBatch;
+    for (int b = blockIdx.x + 1; parts == kJoinBatch; b += kJoinBatch) {
+        parts = 0;
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i)
+            if (b + i < p.ctas && p.key[static_cast<int64_t>(b + i) * p.per] == run) ++parts;  // sorted: the first ones
+        float4 part[kJoinBatch][2];
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) {
+            if (i >= parts) continue;
+            const float4* head = reinterpret_cast<const float4*>(p.head + static_cast<int64_t>(b + i) * p.K + k);
+            part[i][0] = head[0];
+            part[i][1] = head[1];
+        }
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) {
+            if (i >= parts) continue;
+            a[0] += part[i][0].x, a[1] += part[i][0].y, a[2] += part[i][0].z, a[3] += part[i][0].w;
+            a[4] += part[i][1].x, a[5] += part[i][1].y, a[6] += part[i][1].z, a[7] += part[i][1].w;
+        }
+    }
+    float s[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = static_cast<float>(a[j]);
+    embed_store8(p.dtable + static_cast<int64_t>(run) * p.K + k, s, p.scale, p.accumulate);
 }
 
 // ---------------------------------------------------------------------------

@@ -634,7 +634,7 @@ ZeroParams zero_share(ZeroParams* z, int64_t bytes) {
 template <typename Id>
 mmf_status embed_sort(const void* ids, int64_t V, int64_t M, const EmbedPlan& pl, const EmbedWorkspace& w,
                       uint8_t* used, ZeroParams* z, cudaStream_t s) {
-    constexpr int64_t kShareBytes = int64_t(16) << 20;
+    const int64_t share_bytes = (int64_t(24) << 20) + 256 * M;
     for (int i = 0; i < pl.passes; ++i) {
         SortParams p{};
         p.ids = ids;
@@ -651,12 +651,12 @@ mmf_status embed_sort(const void* ids, int64_t V, int64_t M, const EmbedPlan& pl
         p.mask = (1 << pl.digit_bits) - 1;
         p.used = used;
         const dim3 block(kSortThreads);
-        ZeroParams share = zero_share(z, i == 0 ? 0 : kShareBytes);
+        ZeroParams share = zero_share(z, i == 0 ? 0 : share_bytes);
         dim3 grid(static_cast<unsigned>(pl.sort_ctas + embed_zero_ctas(share, kSortThreads)));
         mmf_status st = i == 0 ? launch(embed_count_kernel<Id, true>, grid, block, 0, s, used != nullptr, p, share)
                                : launch(embed_count_kernel<Id, false>, grid, block, 0, s, true, p, share);
         if (st != MMF_OK) return st;
-        share = zero_share(z, kShareBytes);
+        share = zero_share(z, share_bytes);
         grid = dim3(static_cast<unsigned>(pl.sort_ctas + embed_zero_ctas(share, kSortThreads)));
         st = i == 0 ? launch(embed_place_kernel<Id, true>, grid, block, 0, s, true, p, share)
                     : launch(embed_place_kernel<Id, false>, grid, block, 0, s, true, p, share);
@@ -1265,8 +1265,7 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, i
     if ((st = launch(embed_sum_kernel, dim3(static_cast<unsigned>(pl.sum_ctas + embed_zero_ctas(z, pl.threads)), tiles),
                      block, 0, s, true, p, z)) != MMF_OK)
         return st;
-    return launch(embed_join_kernel, dim3(static_cast<unsigned>((pl.sum_ctas + kJoin - 1) / kJoin), tiles), block, 0, s,
-                  true, p);
+    return launch(embed_join_kernel, dim3(static_cast<unsigned>(pl.sum_ctas), tiles), block, 0, s, true, p);
 }
 
 size_t mmf_mlgru_scan_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D) {
