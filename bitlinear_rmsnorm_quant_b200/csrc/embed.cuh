@@ -17,33 +17,61 @@ __device__ __forceinline__ int64_t embed_id(const Id* __restrict__ ids, int64_t 
     return v >= 0 && v < V ? v : -1;
 }
 
-// One CTA per token, 8 columns (16 bytes of x) per thread and step.
+// The rows of x laid end to end in groups of 8 columns (16 bytes), kFwdItems
+// groups per thread, kEmbedThreads apart: all of a thread's ids, then all of
+// its table reads are in flight before the first is used, and any K and M fill
+// the CTAs alike.  x is written past L2 so that the frequent words' rows stay
+// there.
+constexpr int kFwdItems = 4;
+
 template <typename Id, bool BF16>
 __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const Id* __restrict__ ids,
                                                                   const void* __restrict__ table, int64_t V, int64_t M,
                                                                   int K, float scale, uint16_t* __restrict__ x) {
-    for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
-        const int64_t id = embed_id(ids, m, V);
-        for (int k = 8 * threadIdx.x; k < K; k += 8 * kEmbedThreads) {
-            float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-            if (id >= 0) {
-                if (BF16) {
-                    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(table) + id * K + k)), v);
-                } else {
-                    const float4* row = reinterpret_cast<const float4*>(static_cast<const float*>(table) + id * K + k);
-                    const float4 a = __ldg(row), b = __ldg(row + 1);
-                    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-                    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-                }
-            }
-            uint32_t w[4];
+    const unsigned lanes = static_cast<unsigned>(K) / 8;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kFwdItems * kEmbedThreads);
+    const int64_t row0 = first / lanes;
+    const unsigned rest = static_cast<unsigned>(first - row0 * lanes) + threadIdx.x;
+    int64_t id[kFwdItems];
+    bool there[kFwdItems];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(__fmul_rn(v[2 * i], scale), __fmul_rn(v[2 * i + 1], scale));
-                w[i] = *reinterpret_cast<const uint32_t*>(&p);
-            }
-            *reinterpret_cast<uint4*>(x + m * K + k) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int u = 0; u < kFwdItems; ++u) {
+        const int64_t m = row0 + (rest + u * kEmbedThreads) / lanes;
+        there[u] = m < M;
+        id[u] = there[u] ? embed_id(ids, m, V) : -1;
+    }
+    uint4 lo[kFwdItems], hi[kFwdItems];  // 8 bf16, or 8 fp32
+#pragma unroll
+    for (int u = 0; u < kFwdItems; ++u) {
+        lo[u] = hi[u] = make_uint4(0u, 0u, 0u, 0u);
+        const unsigned c = (rest + u * kEmbedThreads) % lanes;
+        if (id[u] < 0) continue;
+        if (BF16) {
+            lo[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(table) + id[u] * K) + c);
+        } else {
+            const uint4* row = reinterpret_cast<const uint4*>(static_cast<const float*>(table) + id[u] * K) + 2 * c;
+            lo[u] = __ldg(row);
+            hi[u] = __ldg(row + 1);
         }
+    }
+#pragma unroll
+    for (int u = 0; u < kFwdItems; ++u) {
+        if (!there[u]) continue;
+        float v[8];
+        if (BF16) {
+            unpack_bf16x8(lo[u], v);
+        } else {
+            v[0] = __uint_as_float(lo[u].x), v[1] = __uint_as_float(lo[u].y), v[2] = __uint_as_float(lo[u].z);
+            v[3] = __uint_as_float(lo[u].w), v[4] = __uint_as_float(hi[u].x), v[5] = __uint_as_float(hi[u].y);
+            v[6] = __uint_as_float(hi[u].z), v[7] = __uint_as_float(hi[u].w);
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(__fmul_rn(v[2 * i], scale), __fmul_rn(v[2 * i + 1], scale));
+            w[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        __stcs(reinterpret_cast<uint4*>(x) + first + threadIdx.x + u * kEmbedThreads, make_uint4(w[0], w[1], w[2], w[3]));
     }
 }
 

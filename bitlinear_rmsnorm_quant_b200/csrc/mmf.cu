@@ -1187,7 +1187,9 @@ int mmf_embed_fwd(const void* ids, const void* table, float scale, int64_t V, in
     DeviceState* dev;
     if ((st = device_state(&dev)) != MMF_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid(static_cast<unsigned>(std::min(M, int64_t(dev->num_sms) * 8))), block(kEmbedThreads);
+    const int64_t ctas = (M * (K / 8) + kFwdItems * kEmbedThreads - 1) / (kFwdItems * kEmbedThreads);
+    if (ctas > kMaxDim) return MMF_ERR_UNSUPPORTED_SHAPE;
+    const dim3 grid(static_cast<unsigned>(ctas)), block(kEmbedThreads);
     const bool wide = (flags & MMF_EMBED_IDS64) != 0, bf16 = (flags & MMF_EMBED_TABLE_BF16) != 0;
     const int k = static_cast<int>(K);
     const int32_t* i32 = static_cast<const int32_t*>(ids);
