@@ -25,8 +25,11 @@ namespace mmf {
 constexpr int kAdamThreads = 256;
 constexpr int kAdamWarps = kAdamThreads / 32;
 constexpr int kAdamBlock = 256;                              // elements that share the scales
-constexpr int kAdamRounds = 2;                               // blocks per warp
-constexpr int kAdamChunk = kAdamWarps * kAdamRounds * kAdamBlock;  // elements per CTA
+constexpr int kAdamRow = kAdamWarps * kAdamBlock;            // elements a CTA takes at once
+// and how often, where there is work for all SMs: 8-bit moments ask for their
+// later rows ahead, 32-bit ones gain nothing from it or from longer chunks
+// (51.4 M elements: 214 us at 2 rounds, 221 at 8, 269 with rows asked for ahead)
+constexpr int kAdamRounds8 = 8, kAdamRounds32 = 2;
 
 // One tensor as the kernel sees it.
 struct AdamTensor {
@@ -41,6 +44,7 @@ struct AdamTensor {
     unsigned long long key;  // of the tensor's noise stream
     float weight_decay;
     int flags;               // kAdam8, kAdamGradBf16
+    int rounds;              // a CTA's chunk of it: rounds * kAdamRow elements
 };
 constexpr int kAdam8 = 1, kAdamGradBf16 = 2;
 
@@ -59,10 +63,22 @@ struct AdamParams {
     int64_t first;              // this launch's first tensor among the call's
 };
 
+// z >> S (S above 16): the upper word's two parts by one multiplication, since
+// the shifts' pipe is the busy one here
+template <int S>
+__host__ __device__ __forceinline__ unsigned long long shift_right(unsigned long long z) {
+#ifdef __CUDA_ARCH__
+    const uint32_t lo = static_cast<uint32_t>(z), hi = static_cast<uint32_t>(z >> 32);
+    return static_cast<unsigned long long>(hi) * (1u << (32 - S)) + (lo >> S);
+#else
+    return z >> S;
+#endif
+}
+
 __host__ __device__ __forceinline__ unsigned long long splitmix_mix(unsigned long long z) {
-    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
-    z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
-    return z ^ (z >> 31);
+    z = (z ^ shift_right<30>(z)) * 0xBF58476D1CE4E5B9ull;
+    z = (z ^ shift_right<27>(z)) * 0x94D049BB133111EBull;
+    return z ^ shift_right<31>(z);
 }
 constexpr unsigned long long kSplitmixGolden = 0x9E3779B97F4A7C15ull;
 
@@ -98,141 +114,237 @@ __device__ __forceinline__ bool adam_scale(uint32_t top, float& scale, float& in
     return held;
 }
 
-// e4m3: 3 mantissa bits, codes 8 .. 126 normal, exponent bias 7 (127 - 7 = 120, 120 << 3 = 960)
-__device__ __forceinline__ uint32_t adam_code_m(float m, float inv, bool held, uint32_t rnd16) {
-    const uint32_t y = __float_as_uint(__fmul_rn(m, inv));
-    const int c = static_cast<int>(((y & 0x7FFFFFFFu) + (rnd16 << 4) + 8u) >> 20) - 960;
-    return held ? static_cast<uint32_t>(c < 8 ? 0 : c) | ((y >> 24) & 0x80u) : 0u;
+// |a|, |b| and c's largest; NaN if one is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
-// e5m2: 2 mantissa bits, codes 4 .. 123 normal, exponent bias 15 (127 - 15 = 112, 112 << 2 = 448)
-__device__ __forceinline__ uint32_t adam_code_v(float v, float inv, bool held, uint32_t rnd16) {
-    const uint32_t y = __float_as_uint(__fmul_rn(v, inv));
-    const int c = static_cast<int>((y + (rnd16 << 5) + 16u) >> 21) - 448;
-    return held && v > 0.0f ? static_cast<uint32_t>(max(c, 4)) : 0u;
+// Bits SHIFT .. SHIFT + 7 (SHIFT 20 or 21) of four words as four bytes.
+template <int SHIFT>
+__device__ __forceinline__ uint32_t pack_bytes(const uint32_t (&t)[4]) {
+    const uint32_t even = __byte_perm(t[0], t[2], 0x7632), odd = __byte_perm(t[1], t[3], 0x7632);  // the upper halves
+    return ((even >> (SHIFT - 16)) & 0x00FF00FFu) | ((odd << (24 - SHIFT)) & 0xFF00FF00u);
 }
 
+// Four e4m3 codes, each the bits of |m| / scale cut to 3 mantissa bits after a
+// random number below a step was added (16 of its 20 bits random, the rest a
+// half).  Bits 20 and up are then the code plus 960 (120, the bias' difference,
+// times 8): its low 7 bits are the code's with bit 6 flipped.  Codes 8 .. 126
+// are normal; below them the code is 0, which few elements are, so a warp looks
+// for them once and not each.
+__device__ __forceinline__ uint32_t adam_codes_m(const float (&m)[4], float inv, const uint32_t (&rnd)[4]) {
+    uint32_t t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        t[e] = __float_as_uint(__fmul_rn(fabsf(m[e]), inv)) + (((rnd[e] << 4) & 0xFFFF0u) | 8u);
+    if (__any_sync(0xffffffffu, min(min(t[0], t[1]), min(t[2], t[3])) < (968u << 20))) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (t[e] < (968u << 20)) t[e] = 0x40u << 20;
+    }
+    const uint32_t signs = __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0073),
+                                       __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0073), 0x5410);
+    return ((pack_bytes<20>(t) & 0x7F7F7F7Fu) | (signs & 0x80808080u)) ^ 0x40404040u;
+}
+
+// Four e5m2 codes, the same with 2 mantissa bits: bits 21 and up are the code
+// plus 448 (112 times 4).  Codes 4 .. 123 are normal; a positive v has at least
+// 4, and 0 is looked for once a warp.
+__device__ __forceinline__ uint32_t adam_codes_v(const float (&v)[4], float inv, const uint32_t (&rnd)[4]) {
+    uint32_t t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        t[e] = max(__float_as_uint(__fmul_rn(v[e], inv)) + (((rnd[e] >> 11) & 0x1FFFE0u) | 16u), 452u << 21);
+    if (__any_sync(0xffffffffu, v[0] == 0.0f || v[1] == 0.0f || v[2] == 0.0f || v[3] == 0.0f)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (v[e] == 0.0f) t[e] = 448u << 21;
+    }
+    return (pack_bytes<21>(t) & 0x7F7F7F7Fu) ^ 0x40404040u;
+}
+
+// a + b of both halves by scalar additions: a packed product and a packed sum
+// behind it come out as one fused operation, which rounds once, not twice
+__device__ __forceinline__ f2 f2_add_unfused(f2 a, f2 b) {
+    const float2 x = f2_get(a), y = f2_get(b);
+    return f2_make(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+}
+
+// One step of two elements.
 struct AdamStep {
-    float beta1, omb1, beta2, omb2, eps, decay, alpha, r, grad_scale;
-    __device__ __forceinline__ void operator()(float& p, float g, float& m, float& v) const {
-        g = __fmul_rn(g, grad_scale);
-        m = __fadd_rn(__fmul_rn(m, beta1), __fmul_rn(g, omb1));
-        v = __fadd_rn(__fmul_rn(v, beta2), __fmul_rn(__fmul_rn(g, g), omb2));
-        float root;
-        asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
-        p = fmaf(-alpha, __fdividef(m, fmaf(root, r, eps)), p * decay);
+    f2 beta1, omb1, beta2, omb2, eps, decay, alpha, r, grad_scale;  // alpha negated
+    __device__ __forceinline__ void operator()(f2& p, f2 g, f2& m, f2& v) const {
+        g = f2_mul(g, grad_scale);
+        m = f2_add_unfused(f2_mul(m, beta1), f2_mul(g, omb1));
+        v = f2_add_unfused(f2_mul(v, beta2), f2_mul(f2_mul(g, g), omb2));
+        float2 root = f2_get(v);
+        asm("sqrt.approx.f32 %0, %0;" : "+f"(root.x));
+        asm("sqrt.approx.f32 %0, %0;" : "+f"(root.y));
+        const float2 d = f2_get(f2_fma(f2_make(root.x, root.y), r, eps));  // at least eps, a normal number
+        float ix, iy;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ix) : "f"(d.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(iy) : "f"(d.y));
+        p = f2_fma(f2_mul(m, f2_make(ix, iy)), alpha, f2_mul(p, decay));
     }
 };
 
 // A block of 256 elements by one warp: lane l has elements 4l .. 4l + 3 of
 // each half, so every access of a full block is one vector per lane over
-// consecutive memory.
-template <bool STATE8, bool GRAD_BF16, bool FULL>
-__device__ __forceinline__ void adam_block(const AdamTensor& t, const AdamStep& step, unsigned long long key,
-                                           int64_t at, int lane) {
-    float p[8], g[8], m[8], v[8];
-    const int left = FULL ? kAdamBlock : static_cast<int>(t.n - at);
-    float ms = 0.0f, vs = 0.0f;
-    if (STATE8) {
-        ms = t.m_scale[at / kAdamBlock];
-        vs = t.v_scale[at / kAdamBlock];
-    }
+// consecutive memory.  AdamRaw is such a block as it lies in memory.
+template <bool STATE8, bool GRAD_BF16>
+struct AdamRaw {
+    float4 p[2];
+    uint4 g[2];  // fp32, or bf16 in x and y
+    uint4 m[2];  // fp32, or 8-bit codes in x
+    uint4 v[2];
+    float ms, vs;
+
+    __device__ __forceinline__ void load(const AdamTensor& t, int64_t at, int lane) {
+        if (STATE8) {
+            ms = t.m_scale[at / kAdamBlock];
+            vs = t.v_scale[at / kAdamBlock];
+        }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int j = 128 * h + 4 * lane;
-        const int64_t i = at + j;
-        float* P = p + 4 * h;
-        float* G = g + 4 * h;
-        float* Mo = m + 4 * h;
-        float* V = v + 4 * h;
-        if (FULL || j + 4 <= left) {
-            const float4 pv = *reinterpret_cast<const float4*>(t.p + i);
-            P[0] = pv.x, P[1] = pv.y, P[2] = pv.z, P[3] = pv.w;
+        for (int h = 0; h < 2; ++h) {
+            const int64_t i = at + 128 * h + 4 * lane;
+            p[h] = *reinterpret_cast<const float4*>(t.p + i);
             if (GRAD_BF16) {
                 const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(t.g) + i);
-                G[0] = __uint_as_float(w.x << 16), G[1] = __uint_as_float(w.x & 0xFFFF0000u);
-                G[2] = __uint_as_float(w.y << 16), G[3] = __uint_as_float(w.y & 0xFFFF0000u);
+                g[h].x = w.x, g[h].y = w.y;
             } else {
-                const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(t.g) + i);
-                G[0] = w.x, G[1] = w.y, G[2] = w.z, G[3] = w.w;
+                g[h] = *reinterpret_cast<const uint4*>(static_cast<const float*>(t.g) + i);
             }
             if (STATE8) {
-                const uint32_t mc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i);
-                const uint32_t vc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i);
-                const float2 a = fp8x2_to_f<false>(mc & 0xFFFFu), b = fp8x2_to_f<false>(mc >> 16);
-                const float2 c = fp8x2_to_f<true>(vc & 0xFFFFu), d = fp8x2_to_f<true>(vc >> 16);
-                Mo[0] = a.x * ms, Mo[1] = a.y * ms, Mo[2] = b.x * ms, Mo[3] = b.y * ms;
-                V[0] = c.x * vs, V[1] = c.y * vs, V[2] = d.x * vs, V[3] = d.y * vs;
+                m[h].x = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i);
+                v[h].x = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i);
             } else {
-                const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(t.m) + i);
-                const float4 c = *reinterpret_cast<const float4*>(static_cast<const float*>(t.v) + i);
-                Mo[0] = a.x, Mo[1] = a.y, Mo[2] = a.z, Mo[3] = a.w;
-                V[0] = c.x, V[1] = c.y, V[2] = c.z, V[3] = c.w;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                P[e] = G[e] = Mo[e] = V[e] = 0.0f;
-                if (j + e < left) {
-                    P[e] = t.p[i + e];
-                    G[e] = GRAD_BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(t.g)[i + e])
-                                     : static_cast<const float*>(t.g)[i + e];
-                    if (STATE8) {
-                        Mo[e] = fp8x2_to_f<false>(static_cast<const uint8_t*>(t.m)[i + e]).x * ms;
-                        V[e] = fp8x2_to_f<true>(static_cast<const uint8_t*>(t.v)[i + e]).x * vs;
-                    } else {
-                        Mo[e] = static_cast<const float*>(t.m)[i + e];
-                        V[e] = static_cast<const float*>(t.v)[i + e];
-                    }
-                }
+                m[h] = *reinterpret_cast<const uint4*>(static_cast<const float*>(t.m) + i);
+                v[h] = *reinterpret_cast<const uint4*>(static_cast<const float*>(t.v) + i);
             }
         }
     }
-    uint32_t mtop = 0, vtop = 0;
+};
+
+// Its elements as fp32 pairs, two of each half.
+struct AdamValues {
+    f2 p[4], g[4], m[4], v[4];
+
+    template <bool STATE8, bool GRAD_BF16>
+    __device__ __forceinline__ void unpack(const AdamRaw<STATE8, GRAD_BF16>& r) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        step(p[e], g[e], m[e], v[e]);
-        if (STATE8 && (FULL || (e / 4) * 128 + 4 * lane + (e & 3) < left)) {
-            mtop = max(mtop, __float_as_uint(m[e]) & 0x7FFFFFFFu);
-            vtop = max(vtop, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        for (int h = 0; h < 2; ++h) {
+            p[2 * h] = f2_make(r.p[h].x, r.p[h].y), p[2 * h + 1] = f2_make(r.p[h].z, r.p[h].w);
+            if (GRAD_BF16) {
+                g[2 * h] = f2_make(__uint_as_float(r.g[h].x << 16), __uint_as_float(r.g[h].x & 0xFFFF0000u));
+                g[2 * h + 1] = f2_make(__uint_as_float(r.g[h].y << 16), __uint_as_float(r.g[h].y & 0xFFFF0000u));
+            } else {
+                words(g + 2 * h, r.g[h]);
+            }
+            if (STATE8) {
+                const float2 a = fp8x2_to_f<false>(r.m[h].x & 0xFFFFu), b = fp8x2_to_f<false>(r.m[h].x >> 16);
+                const float2 c = fp8x2_to_f<true>(r.v[h].x & 0xFFFFu), d = fp8x2_to_f<true>(r.v[h].x >> 16);
+                const f2 ms = f2_set(r.ms), vs = f2_set(r.vs);
+                m[2 * h] = f2_mul(f2_make(a.x, a.y), ms), m[2 * h + 1] = f2_mul(f2_make(b.x, b.y), ms);
+                v[2 * h] = f2_mul(f2_make(c.x, c.y), vs), v[2 * h + 1] = f2_mul(f2_make(d.x, d.y), vs);
+            } else {
+                words(m + 2 * h, r.m[h]);
+                words(v + 2 * h, r.v[h]);
+            }
         }
+    }
+    static __device__ __forceinline__ void words(f2* to, const uint4& w) {
+        to[0] = f2_make(__uint_as_float(w.x), __uint_as_float(w.y));
+        to[1] = f2_make(__uint_as_float(w.z), __uint_as_float(w.w));
+    }
+
+    // a tensor's last, short block: `left` elements, the others zeros
+    template <bool STATE8, bool GRAD_BF16>
+    __device__ __forceinline__ void load_short(const AdamTensor& t, int64_t at, int left, int lane) {
+        const float ms = STATE8 ? t.m_scale[at / kAdamBlock] : 0.0f, vs = STATE8 ? t.v_scale[at / kAdamBlock] : 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float e[4][2] = {};
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int j = 128 * (q / 2) + 4 * lane + 2 * (q & 1) + s;
+                if (j >= left) continue;
+                e[0][s] = t.p[at + j];
+                e[1][s] = GRAD_BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(t.g)[at + j])
+                                    : static_cast<const float*>(t.g)[at + j];
+                e[2][s] = STATE8 ? fp8x2_to_f<false>(static_cast<const uint8_t*>(t.m)[at + j]).x * ms
+                                 : static_cast<const float*>(t.m)[at + j];
+                e[3][s] = STATE8 ? fp8x2_to_f<true>(static_cast<const uint8_t*>(t.v)[at + j]).x * vs
+                                 : static_cast<const float*>(t.v)[at + j];
+            }
+            p[q] = f2_make(e[0][0], e[0][1]);
+            g[q] = f2_make(e[1][0], e[1][1]);
+            m[q] = f2_make(e[2][0], e[2][1]);
+            v[q] = f2_make(e[3][0], e[3][1]);
+        }
+    }
+};
+
+// The step of a block's elements, and their way back to memory.
+template <bool STATE8, bool FULL>
+__device__ __forceinline__ void adam_block(const AdamTensor& t, const AdamStep& step, unsigned long long key,
+                                           AdamValues& x, int64_t at, int left, int lane) {
+    float me[8], ve[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        step(x.p[q], x.g[q], x.m[q], x.v[q]);
+        const float2 a = f2_get(x.m[q]), b = f2_get(x.v[q]);
+        me[2 * q] = a.x, me[2 * q + 1] = a.y;
+        ve[2 * q] = b.x, ve[2 * q + 1] = b.y;
     }
     float minv = 0.0f, vinv = 0.0f;
     bool mheld = true, vheld = true;
+    unsigned long long draw = 0;
     if (STATE8) {
-        mtop = __reduce_max_sync(0xffffffffu, mtop);
-        vtop = __reduce_max_sync(0xffffffffu, vtop);
+        if (!FULL) {  // the places behind the end count for nothing, whatever 0 * grad_scale is
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if ((e / 4) * 128 + 4 * lane + (e & 3) >= left) me[e] = ve[e] = 0.0f;
+        }
+        float ml = 0.0f, vl = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            ml = max3_abs(me[e], me[e + 1], ml);
+            vl = max3_abs(ve[e], ve[e + 1], vl);
+        }
+        const uint32_t mtop = __reduce_max_sync(0xffffffffu, __float_as_uint(ml));
+        const uint32_t vtop = __reduce_max_sync(0xffffffffu, __float_as_uint(vl));
+        float ms, vs;
         mheld = adam_scale<7>(mtop, ms, minv);
         vheld = adam_scale<14>(vtop, vs, vinv);
         if (lane == 0) {
             t.m_scale[at / kAdamBlock] = ms;
             t.v_scale[at / kAdamBlock] = vs;
         }
+        // element i takes half of draw i / 2 of the stream, m the low 16 bits of it
+        draw = key + (static_cast<unsigned long long>(at / 2) + 2 * lane + 1) * kSplitmixGolden;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int j = 128 * h + 4 * lane;
         const int64_t i = at + j;
-        const float* P = p + 4 * h;
+        const float2 p0 = f2_get(x.p[2 * h]), p1 = f2_get(x.p[2 * h + 1]);
+        const float M4[4] = {me[4 * h], me[4 * h + 1], me[4 * h + 2], me[4 * h + 3]};
+        const float V4[4] = {ve[4 * h], ve[4 * h + 1], ve[4 * h + 2], ve[4 * h + 3]};
         uint32_t mc = 0, vc = 0;
         if (STATE8) {
-            // draws i / 2 and i / 2 + 1 of the stream: 32 bits per element, m below v
-#pragma unroll
-            for (int d = 0; d < 2; ++d) {
-                const unsigned long long z =
-                    splitmix_mix(key + (static_cast<unsigned long long>(i / 2) + d + 1) * kSplitmixGolden);
-                const uint32_t lo = static_cast<uint32_t>(z), hi = static_cast<uint32_t>(z >> 32);
-                const int e = 4 * h + 2 * d;
-                mc |= (adam_code_m(m[e], minv, mheld, lo & 0xFFFFu) | (adam_code_m(m[e + 1], minv, mheld, hi & 0xFFFFu) << 8))
-                      << (16 * d);
-                vc |= (adam_code_v(v[e], vinv, vheld, lo >> 16) | (adam_code_v(v[e + 1], vinv, vheld, hi >> 16) << 8))
-                      << (16 * d);
-            }
+            const unsigned long long z0 = splitmix_mix(draw + (64 * h) * kSplitmixGolden);
+            const unsigned long long z1 = splitmix_mix(draw + (64 * h + 1) * kSplitmixGolden);
+            const uint32_t rnd[4] = {static_cast<uint32_t>(z0), static_cast<uint32_t>(z0 >> 32), static_cast<uint32_t>(z1),
+                                     static_cast<uint32_t>(z1 >> 32)};
+            mc = mheld ? adam_codes_m(M4, minv, rnd) : 0u;
+            vc = vheld ? adam_codes_v(V4, vinv, rnd) : 0u;
         }
         if (FULL || j + 4 <= left) {
-            *reinterpret_cast<float4*>(t.p + i) = make_float4(P[0], P[1], P[2], P[3]);
+            *reinterpret_cast<float4*>(t.p + i) = make_float4(p0.x, p0.y, p1.x, p1.y);
             if (t.p_bf16) {
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(P[0], P[1]), hi = __floats2bfloat162_rn(P[2], P[3]);
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(p0.x, p0.y), hi = __floats2bfloat162_rn(p1.x, p1.y);
                 *reinterpret_cast<uint2*>(t.p_bf16 + i) =
                     make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
             }
@@ -240,50 +352,75 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, const AdamStep& 
                 *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + i) = mc;
                 *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + i) = vc;
             } else {
-                *reinterpret_cast<float4*>(static_cast<float*>(t.m) + i) =
-                    make_float4(m[4 * h], m[4 * h + 1], m[4 * h + 2], m[4 * h + 3]);
-                *reinterpret_cast<float4*>(static_cast<float*>(t.v) + i) =
-                    make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+                *reinterpret_cast<float4*>(static_cast<float*>(t.m) + i) = make_float4(M4[0], M4[1], M4[2], M4[3]);
+                *reinterpret_cast<float4*>(static_cast<float*>(t.v) + i) = make_float4(V4[0], V4[1], V4[2], V4[3]);
             }
         } else {
+            const float P4[4] = {p0.x, p0.y, p1.x, p1.y};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (j + e >= left) continue;
-                t.p[i + e] = P[e];
+                t.p[i + e] = P4[e];
                 if (t.p_bf16) {
-                    const __nv_bfloat16 q = __float2bfloat16_rn(P[e]);
+                    const __nv_bfloat16 q = __float2bfloat16_rn(P4[e]);
                     t.p_bf16[i + e] = *reinterpret_cast<const uint16_t*>(&q);
                 }
                 if (STATE8) {
                     static_cast<uint8_t*>(t.m)[i + e] = static_cast<uint8_t>(mc >> (8 * e));
                     static_cast<uint8_t*>(t.v)[i + e] = static_cast<uint8_t>(vc >> (8 * e));
                 } else {
-                    static_cast<float*>(t.m)[i + e] = m[4 * h + e];
-                    static_cast<float*>(t.v)[i + e] = v[4 * h + e];
+                    static_cast<float*>(t.m)[i + e] = M4[e];
+                    static_cast<float*>(t.v)[i + e] = V4[e];
                 }
             }
         }
     }
 }
 
+// Brings a row of kAdamRow elements into L2, by one thread.  A CTA's later rows
+// are asked for kAdamAhead rows before they are worked on: the loads then wait
+// for L2 only, and HBM is kept busy whatever the warps do.
+constexpr int kAdamAhead = 2;
+
+template <bool STATE8, bool GRAD_BF16>
+__device__ __forceinline__ void adam_prefetch(const AdamTensor& t, int64_t at) {
+    if (at + kAdamRow > t.n) return;
+    bulk_prefetch_l2(t.p + at, 4 * kAdamRow);
+    bulk_prefetch_l2(static_cast<const uint8_t*>(t.g) + (GRAD_BF16 ? 2 : 4) * at, (GRAD_BF16 ? 2 : 4) * kAdamRow);
+    bulk_prefetch_l2(static_cast<const uint8_t*>(t.m) + (STATE8 ? 1 : 4) * at, (STATE8 ? 1 : 4) * kAdamRow);
+    bulk_prefetch_l2(static_cast<const uint8_t*>(t.v) + (STATE8 ? 1 : 4) * at, (STATE8 ? 1 : 4) * kAdamRow);
+}
+
+// A CTA's chunk: `rounds` blocks per warp, kAdamRow apart.
 template <bool STATE8, bool GRAD_BF16>
 __device__ __forceinline__ void adam_chunk(const AdamTensor& t, const AdamStep& step, unsigned long long key,
-                                           int64_t chunk) {
+                                           int64_t chunk, int rounds) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-    for (int r = 0; r < kAdamRounds; ++r) {
-        const int64_t at = chunk * kAdamChunk + (r * kAdamWarps + warp) * kAdamBlock;
-        if (at + kAdamBlock <= t.n)
-            adam_block<STATE8, GRAD_BF16, true>(t, step, key, at, lane);
-        else if (at < t.n)
-            adam_block<STATE8, GRAD_BF16, false>(t, step, key, at, lane);
+    const int64_t row = chunk * rounds * kAdamRow;
+    if (STATE8 && threadIdx.x == 0)
+        for (int r = 1; r <= kAdamAhead && r < rounds; ++r) adam_prefetch<STATE8, GRAD_BF16>(t, row + r * kAdamRow);
+    for (int r = 0; r < rounds; ++r) {
+        if (STATE8 && threadIdx.x == 0 && r + 1 + kAdamAhead < rounds)
+            adam_prefetch<STATE8, GRAD_BF16>(t, row + (r + 1 + kAdamAhead) * kAdamRow);
+        const int64_t at = row + r * kAdamRow + warp * kAdamBlock;
+        AdamValues x;
+        if (at + kAdamBlock <= t.n) {
+            AdamRaw<STATE8, GRAD_BF16> raw;
+            raw.load(t, at, lane);
+            x.unpack(raw);
+            adam_block<STATE8, true>(t, step, key, x, at, kAdamBlock, lane);
+        } else if (at < t.n) {
+            const int left = static_cast<int>(t.n - at);
+            x.load_short<STATE8, GRAD_BF16>(t, at, left, lane);
+            adam_block<STATE8, false>(t, step, key, x, at, left, lane);
+        }
     }
 }
 
 // CTA c takes chunk c of the call's tensors laid end to end, each tensor's
 // chunks beginning with its first element.
 template <int CAP>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamParams<CAP> p) {
+__global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_constant__ AdamParams<CAP> p) {
     int lo = 0, hi = p.count;  // chunk_start[lo] <= blockIdx.x < chunk_start[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -301,15 +438,16 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
                        static_cast<unsigned long long>(p.first + lo));
     }
     AdamStep step;
-    step.beta1 = p.beta1, step.omb1 = p.omb1, step.beta2 = p.beta2, step.omb2 = p.omb2, step.eps = p.eps;
-    step.decay = __fsub_rn(1.0f, __fmul_rn(s.lr, t.weight_decay));
-    step.alpha = s.alpha, step.r = s.r, step.grad_scale = s.grad_scale;
+    step.beta1 = f2_set(p.beta1), step.omb1 = f2_set(p.omb1);
+    step.beta2 = f2_set(p.beta2), step.omb2 = f2_set(p.omb2), step.eps = f2_set(p.eps);
+    step.decay = f2_set(__fsub_rn(1.0f, __fmul_rn(s.lr, t.weight_decay)));
+    step.alpha = f2_set(-s.alpha), step.r = f2_set(s.r), step.grad_scale = f2_set(s.grad_scale);
     const int64_t chunk = blockIdx.x - p.chunk_start[lo];
     switch (t.flags) {
-        case 0: adam_chunk<false, false>(t, step, key, chunk); break;
-        case kAdamGradBf16: adam_chunk<false, true>(t, step, key, chunk); break;
-        case kAdam8: adam_chunk<true, false>(t, step, key, chunk); break;
-        default: adam_chunk<true, true>(t, step, key, chunk); break;
+        case 0: adam_chunk<false, false>(t, step, key, chunk, t.rounds); break;
+        case kAdamGradBf16: adam_chunk<false, true>(t, step, key, chunk, t.rounds); break;
+        case kAdam8: adam_chunk<true, false>(t, step, key, chunk, t.rounds); break;
+        default: adam_chunk<true, true>(t, step, key, chunk, t.rounds); break;
     }
 }
 

@@ -765,7 +765,7 @@ mmf_status adam_scalars(const mmf_adamw_hyper* h, mmf_adamw_scalars* out) {
         !std::isfinite(static_cast<float>(h->grad_scale)))
         return MMF_ERR_INVALID_ARG;
     // what the kernel uses is fp32: an eps or a beta that rounds out of its range is refused too
-    if (!(static_cast<float>(h->eps) > 0.0f) || static_cast<float>(h->beta1) >= 1.0f ||
+    if (!(static_cast<float>(h->eps) >= 1.17549435e-38f) || static_cast<float>(h->beta1) >= 1.0f ||
         static_cast<float>(h->beta2) >= 1.0f)
         return MMF_ERR_INVALID_ARG;
     const double t = static_cast<double>(h->step);
@@ -833,14 +833,19 @@ template <int CAP>
 mmf_status launch_adamw(const mmf_adamw_tensor* tensors, int first, int count, const mmf_adamw_hyper* h,
                         const mmf_adamw_scalars& sc, const mmf_adamw_scalars* scalars, cudaStream_t s) {
     AdamParams<CAP> p;
-    int64_t chunks = 0;
+    // as many blocks per warp as still leave every SM a few CTAs
+    int64_t rows = 0, chunks = 0;
+    for (int i = 0; i < count; ++i) rows += (tensors[first + i].n + kAdamRow - 1) / kAdamRow;
+    const int rounds = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kAdamRounds8, rows / (148 * 8))));
     for (int i = 0; i < count; ++i) {
         const mmf_adamw_tensor& t = tensors[first + i];
         p.t[i] = {t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.p_bf16, t.n,
                   adam_key(sc.seed, static_cast<unsigned long long>(first + i)), t.weight_decay,
-                  ((t.flags & MMF_ADAMW_STATE8) ? kAdam8 : 0) | ((t.flags & MMF_ADAMW_GRAD_BF16) ? kAdamGradBf16 : 0)};
+                  ((t.flags & MMF_ADAMW_STATE8) ? kAdam8 : 0) | ((t.flags & MMF_ADAMW_GRAD_BF16) ? kAdamGradBf16 : 0),
+                  (t.flags & MMF_ADAMW_STATE8) ? rounds : std::min(rounds, kAdamRounds32)};
+        const int64_t chunk = int64_t(p.t[i].rounds) * kAdamRow;
         p.chunk_start[i] = static_cast<unsigned>(chunks);
-        chunks += (t.n + kAdamChunk - 1) / kAdamChunk;
+        chunks += (t.n + chunk - 1) / chunk;
         if (chunks > kMaxDim) return MMF_ERR_UNSUPPORTED_SHAPE;
     }
     if (chunks == 0) return MMF_OK;

@@ -31,36 +31,6 @@ namespace mmf {
 constexpr int kSbSub = 8;      // tokens taken backwards at a time
 constexpr int kSbWarps = 4;    // warps per CTA, each on a segment of its own
 
-// A channel pair's fp32 values, computed two at a time (packed fp32 pairs).
-typedef unsigned long long f2;
-
-__device__ __forceinline__ f2 f2_make(float lo, float hi) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 f2_get(f2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 f2_set(float v) { return f2_make(v, v); }
-
 // a bf16 pair -> fp32 pair
 __device__ __forceinline__ f2 f2_bf16(uint32_t w) {
     return f2_make(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));

@@ -312,7 +312,7 @@ int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre,
  * not overlap one another (checked, MMF_ERR_INVALID_ARG) nor any g.  Launches
  * one kernel per 256 tensors.
  *
- * hyper: HOST struct, read during the call only.  0 <= beta < 1, eps > 0,
+ * hyper: HOST struct, read during the call only.  0 <= beta < 1, eps >= 2^-126,
  * lr >= 0, step >= 1 (the count that includes this step), everything finite.
  * scalars: NULL, or a DEVICE copy (16-byte aligned) of what
  * mmf_adamw_scalars_at fills: the kernel then takes lr, the bias corrections,
