@@ -452,6 +452,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const SumPara
 // ---------------------------------------------------------------------------
 constexpr int kFewTokens = 1024;
 constexpr int kFewGroup = 64;
+constexpr int kFewBatch = 16;  // rows of dx in flight per thread
 
 template <typename Id>
 __global__ void __launch_bounds__(kEmbedThreads) embed_few_kernel(const Id* __restrict__ ids,
@@ -486,13 +487,13 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_few_kernel(const Id* __re
     for (int g = 0; g < count; g += kFewGroup) {
         const int end = min(count, g + kFewGroup);
         float a[8] = {};
-        for (int i0 = g; i0 < end; i0 += kSumBatch) {
-            uint4 row[kSumBatch];
+        for (int i0 = g; i0 < end; i0 += kFewBatch) {
+            uint4 row[kFewBatch];
 #pragma unroll
-            for (int u = 0; u < kSumBatch; ++u)
+            for (int u = 0; u < kFewBatch; ++u)
                 if (i0 + u < end) row[u] = __ldg(reinterpret_cast<const uint4*>(dx + static_cast<int64_t>(pos[i0 + u]) * K + k));
 #pragma unroll
-            for (int u = 0; u < kSumBatch; ++u) {
+            for (int u = 0; u < kFewBatch; ++u) {
                 if (i0 + u >= end) break;
                 float v[8];
                 unpack_bf16x8(row[u], v);

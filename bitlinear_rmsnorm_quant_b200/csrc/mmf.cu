@@ -678,14 +678,25 @@ mmf_status check_scan_shape(int64_t B, int64_t T, int64_t D) {
 // of resident CTAs shortest, a CTA's time being its steps, about two steps to
 // begin and end, and 0.15 steps for each other segment whose map it folds.
 struct ScanBwdPlan {
-    bool tma;
+    bool one_launch, tma;
     int gw, groups, subs, subs_per_seg, segments;
 };
 
 ScanBwdPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D) {
-    ScanBwdPlan pl;
-    pl.tma = D % 8 == 0 && D >= 64 && T >= kSbSub && 2 * T * D < (int64_t(1) << 40);
+    ScanBwdPlan pl{};
     const int64_t tiles = (D + 63) / 64;
+    // where one wave of single warps holds the channels of all (short) sequences,
+    // a second launch costs more than it splits (37 tokens of 1022 channels: 22.8 us
+    // a call with two launches, 17.5 with one)
+    pl.one_launch = T <= kSbShort && B * tiles <= int64_t(148) * 16;
+    if (pl.one_launch) {
+        pl.groups = static_cast<int>(tiles);
+        pl.subs = pl.subs_per_seg = static_cast<int>((T + kSbSub - 1) / kSbSub);
+        pl.segments = 1;
+        pl.gw = 1;
+        return pl;
+    }
+    pl.tma = D % 8 == 0 && D >= 64 && T >= kSbSub && 2 * T * D < (int64_t(1) << 40);
     pl.gw = 1;
     if (pl.tma)  // the widest CTA that wastes no more than a quarter of its channels
         for (int gw = 2; gw <= kSbMaxGw; ++gw)
@@ -740,8 +751,9 @@ struct ScanBwdWorkspace {
 ScanBwdWorkspace carve_scan_bwd(void* ws, const ScanBwdPlan& pl, int64_t B, int64_t D) {
     uint8_t* b = static_cast<uint8_t*>(ws);
     const size_t row = static_cast<size_t>(B) * static_cast<size_t>(D) / 2;
-    ScanBwdWorkspace w;
+    ScanBwdWorkspace w{};
     size_t at = 0;
+    if (pl.one_launch) return w;
     w.part = reinterpret_cast<float4*>(b + at);
     at += align256(row * pl.subs * sizeof(float4));
     w.seg = reinterpret_cast<float4*>(b + at);
@@ -1342,6 +1354,7 @@ int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre, const uint1
         }
     }
     const dim3 grid(static_cast<unsigned>((p.items + kSbWarps - 1) / kSbWarps)), block(kSbWarps * 32);
+    if (pl.one_launch) return launch(mlgru_scan_bwd_short_kernel, grid, block, 0, s, false, p);
     if ((st = launch(mlgru_scan_bwd_maps_kernel, grid, block, 0, s, false, p)) != MMF_OK) return st;
     return launch(mlgru_scan_bwd_kernel, grid, block, 0, s, true, p);
 }

@@ -141,7 +141,47 @@ __global__ void __launch_bounds__(kSbWarps * 32) mlgru_scan_bwd_maps_kernel(cons
     p.seg_r[to] = r;
 }
 
-__global__ void __launch_bounds__(kSbWarps * 32, 4) mlgru_scan_bwd_kernel(const ScanBwdParams p) {
+// n (at most kSbSub) tokens from element `at` on, taken backwards: hs is the
+// state before them, dh the gradient of the state behind them and then of hs.
+__device__ __forceinline__ void scan_back(const ScanBwdParams& p, int64_t at, int n, f2 hs, f2& dh) {
+    uint32_t wf[kSbSub], wc[kSbSub], wg[kSbSub], wd[kSbSub];
+#pragma unroll
+    for (int i = 0; i < kSbSub; ++i) {
+        const int64_t o = at + static_cast<int64_t>(i) * p.D;
+        const bool there = i < n;
+        wf[i] = there ? ld_pair(p.f_pre + o) : 0u;
+        wc[i] = there ? ld_pair(p.c_pre + o) : 0u;
+        wg[i] = there ? ld_pair(p.g_pre + o) : 0u;
+        wd[i] = there ? ld_pair(p.d_o + o) : 0u;
+    }
+    // of each token: what dh is multiplied with for df_pre, dc_pre and the token before, and do g
+    f2 xf[kSbSub], xc[kSbSub], fg[kSbSub], dg[kSbSub];
+#pragma unroll
+    for (int i = 0; i < kSbSub; ++i) {
+        if (i >= n) break;
+        const ScanGates t(wf[i], wc[i], wg[i]);
+        const f2 omf = f2_mul(t.ef, t.f);   // 1 - f
+        const f2 c = f2_mul(t.cp, t.s);
+        xf[i] = f2_mul(f2_fma(c, f2_set(-1.0f), hs), f2_mul(t.f, omf));
+        xc[i] = f2_mul(omf, f2_mul(t.s, f2_fma(t.cp, f2_mul(t.ec, t.s), f2_set(1.0f))));
+        hs = f2_fma(t.f, hs, f2_mul(omf, c));
+        fg[i] = t.f;
+        dg[i] = f2_mul(f2_bf16(wd[i]), t.g);
+        *reinterpret_cast<uint32_t*>(p.dg_pre + at + static_cast<int64_t>(i) * p.D) =
+            f2_to_bf16(f2_mul(f2_mul(dg[i], hs), f2_mul(t.eg, t.g)));
+    }
+#pragma unroll
+    for (int i = kSbSub - 1; i >= 0; --i) {
+        if (i >= n) continue;
+        const int64_t o = at + static_cast<int64_t>(i) * p.D;
+        const f2 d = f2_add(dg[i], dh);
+        *reinterpret_cast<uint32_t*>(p.df_pre + o) = f2_to_bf16(f2_mul(d, xf[i]));
+        *reinterpret_cast<uint32_t*>(p.dc_pre + o) = f2_to_bf16(f2_mul(d, xc[i]));
+        dh = f2_mul(d, fg[i]);
+    }
+}
+
+__global__ void __launch_bounds__(kSbWarps * 32, 3) mlgru_scan_bwd_kernel(const ScanBwdParams p) {
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kSbWarps + (threadIdx.x >> 5);
     if (item >= p.items) return;
     // the last segments first: the maps kernel has just read them
@@ -170,49 +210,57 @@ __global__ void __launch_bounds__(kSbWarps * 32, 4) mlgru_scan_bwd_kernel(const 
     }
     for (int sub = sub1 - 1; sub >= sub0; --sub) {
         const int t0 = sub * kSbSub;
-        const int64_t at = (it.b * p.T + t0) * p.D + it.k;
-        const int n = min(kSbSub, p.T - t0);
         const float4 m = p.part[(it.b * p.subs + sub) * half + it.k / 2];
-        uint32_t wf[kSbSub], wc[kSbSub], wg[kSbSub], wd[kSbSub];
+        scan_back(p, (it.b * p.T + t0) * p.D + it.k, min(kSbSub, p.T - t0),
+                  f2_fma(f2_make(m.x, m.y), h, f2_make(m.z, m.w)), dh);
+    }
+    if (p.dh0 && it.seg == 0) *reinterpret_cast<float2*>(p.dh0 + it.b * p.D + it.k) = f2_get(dh);
+}
+
+// Short sequences (kSbShort tokens at most) in one launch: a warp walks its 64
+// channels' tokens forward, keeping the state before every kSbSub-th in shared
+// memory, and takes them backwards from there.
+constexpr int kSbShort = 64;
+
+__global__ void __launch_bounds__(kSbWarps * 32, 3) mlgru_scan_bwd_short_kernel(const ScanBwdParams p) {
+    __shared__ float2 kept[kSbWarps][kSbShort / kSbSub][32];
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * kSbWarps + (threadIdx.x >> 5);
+    if (item >= p.items) return;
+    const ScanItem it(p, item);  // S = 1
+    if (!it.valid) return;
+    const int lane = threadIdx.x & 31;
+    float2(*keep)[32] = kept[threadIdx.x >> 5];
+    f2 h = f2_set(0.0f), dh = f2_set(0.0f);
+    if (p.h0) h = *reinterpret_cast<const f2*>(p.h0 + it.b * p.D + it.k);
+    if (p.dh_last) dh = *reinterpret_cast<const f2*>(p.dh_last + it.b * p.D + it.k);
+    const int64_t base = it.b * p.T * p.D + it.k;
+    for (int sub = 0; sub < p.subs; ++sub) {
+        keep[sub][lane] = f2_get(h);
+        const int n = min(kSbSub, p.T - sub * kSbSub);
+        const int64_t at = base + static_cast<int64_t>(sub) * kSbSub * p.D;
+        uint32_t wf[kSbSub], wc[kSbSub];
 #pragma unroll
         for (int i = 0; i < kSbSub; ++i) {
-            const int64_t o = at + static_cast<int64_t>(i) * p.D;
-            const bool there = i < n;
-            wf[i] = there ? ld_pair(p.f_pre + o) : 0u;
-            wc[i] = there ? ld_pair(p.c_pre + o) : 0u;
-            wg[i] = there ? ld_pair(p.g_pre + o) : 0u;
-            wd[i] = there ? ld_pair(p.d_o + o) : 0u;
+            wf[i] = i < n ? ld_pair(p.f_pre + at + static_cast<int64_t>(i) * p.D) : 0u;
+            wc[i] = i < n ? ld_pair(p.c_pre + at + static_cast<int64_t>(i) * p.D) : 0u;
         }
-        f2 hs = f2_fma(f2_make(m.x, m.y), h, f2_make(m.z, m.w));  // the state before these tokens
-        // of each token: what dh is multiplied with for df_pre, dc_pre and the token before, and do g
-        f2 xf[kSbSub], xc[kSbSub], fg[kSbSub], dg[kSbSub];
 #pragma unroll
         for (int i = 0; i < kSbSub; ++i) {
             if (i >= n) break;
-            const ScanGates t(wf[i], wc[i], wg[i]);
-            const f2 one = f2_set(1.0f);
-            const f2 d_o = f2_bf16(wd[i]);
-            const f2 omf = f2_mul(t.ef, t.f);   // 1 - f
-            const f2 c = f2_mul(t.cp, t.s);
-            xf[i] = f2_mul(f2_fma(c, f2_set(-1.0f), hs), f2_mul(t.f, omf));
-            xc[i] = f2_mul(omf, f2_mul(t.s, f2_fma(t.cp, f2_mul(t.ec, t.s), one)));
-            hs = f2_fma(t.f, hs, f2_mul(omf, c));
-            fg[i] = t.f;
-            dg[i] = f2_mul(d_o, t.g);
-            *reinterpret_cast<uint32_t*>(p.dg_pre + at + static_cast<int64_t>(i) * p.D) =
-                f2_to_bf16(f2_mul(f2_mul(dg[i], hs), f2_mul(t.eg, t.g)));
-        }
-#pragma unroll
-        for (int i = kSbSub - 1; i >= 0; --i) {
-            if (i >= n) continue;
-            const int64_t o = at + static_cast<int64_t>(i) * p.D;
-            const f2 d = f2_add(dg[i], dh);
-            *reinterpret_cast<uint32_t*>(p.df_pre + o) = f2_to_bf16(f2_mul(d, xf[i]));
-            *reinterpret_cast<uint32_t*>(p.dc_pre + o) = f2_to_bf16(f2_mul(d, xc[i]));
-            dh = f2_mul(d, fg[i]);
+            const f2 cp = f2_bf16(clamp_bf16x2(wc[i])), ef = f2_exp_neg(f2_bf16(clamp_bf16x2(wf[i])));
+            const f2 df = f2_add(f2_set(1.0f), ef), dc = f2_add(f2_set(1.0f), f2_exp_neg(cp));
+            const float2 d = f2_get(f2_mul(df, dc));
+            const f2 r = f2_make(rcp_ftz(d.x), rcp_ftz(d.y));
+            const f2 f = f2_mul(r, dc);
+            h = f2_fma(f, h, f2_mul(f2_mul(ef, f), f2_mul(cp, f2_mul(r, df))));
         }
     }
-    if (p.dh0 && it.seg == 0) *reinterpret_cast<float2*>(p.dh0 + it.b * p.D + it.k) = f2_get(dh);
+    for (int sub = p.subs - 1; sub >= 0; --sub) {
+        const float2 hs = keep[sub][lane];
+        scan_back(p, base + static_cast<int64_t>(sub) * kSbSub * p.D, min(kSbSub, p.T - sub * kSbSub),
+                  f2_make(hs.x, hs.y), dh);
+    }
+    if (p.dh0) *reinterpret_cast<float2*>(p.dh0 + it.b * p.D + it.k) = f2_get(dh);
 }
 
 // ---------------------------------------------------------------------------

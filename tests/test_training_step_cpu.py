@@ -122,8 +122,9 @@ def test_embed_argument_errors(L):
 
 def test_scan_bwd_argument_errors(L):
     f = L.mmf_mlgru_scan_bwd
-    need = L.mmf_mlgru_scan_bwd_workspace_bytes(1, 4, 64)
-    ok = [A, A, A, A, None, None, 1, 4, 64, A, A, A, None, A, need, None]
+    need = L.mmf_mlgru_scan_bwd_workspace_bytes(1, 400, 64)
+    assert need > 0 and L.mmf_mlgru_scan_bwd_workspace_bytes(1, 0, 64) == 0
+    ok = [A, A, A, A, None, None, 1, 400, 64, A, A, A, None, A, need, None]
 
     def but(**at):
         a = list(ok)
@@ -140,8 +141,7 @@ def test_scan_bwd_argument_errors(L):
         assert but(**{f"_{i}": MIS}) == 3
     for i in (4, 5, 12, 13):
         assert but(**{f"_{i}": MIS}) == 3
-    if need:
-        assert but(_13=None) == 4 and but(_14=need - 1) == 4
+    assert but(_13=None) == 4 and but(_14=need - 1) == 4
     assert but(_6=0) == 0 and but(_8=0) == 0
     assert but(_7=0) == 0                                         # no tokens and no dh0 wanted
 

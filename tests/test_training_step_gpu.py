@@ -120,7 +120,9 @@ def test_embed_infinities_stay_in_their_rows():
 # -- gradient of the recurrence ----------------------------------------------------
 
 SCAN_SHAPES = [(1, 1, 2), (1, 1, 2560), (2, 37, 128), (3, 100, 66), (1, 37, 1022), (2, 5, 64), (3, 8, 62), (1, 300, 200),
-               (2, 16, 4104), (2, 129, 512), (5, 70, 34), (1, 1000, 72), (2, 2048, 8), (1, 4099, 24), (70, 3, 6)]
+               (2, 16, 4104), (2, 129, 512), (5, 70, 34), (1, 1000, 72), (2, 2048, 8), (1, 4099, 24), (70, 3, 6),
+               # 64 tokens and one more; short sequences of more channels than one launch of single warps holds
+               (1, 64, 96), (1, 65, 96), (2400, 5, 6), (2400, 9, 64), (600, 64, 264)]
 
 
 @pytest.mark.parametrize("B,T,D", SCAN_SHAPES)
