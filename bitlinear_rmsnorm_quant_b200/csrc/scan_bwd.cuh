@@ -455,12 +455,14 @@ __global__ void __launch_bounds__(GW * 32, 16 / GW) mlgru_scan_bwd_tma_kernel(co
     }
     const float4* part = p.part + (static_cast<int64_t>(at.b) * p.subs + at.sub1 - 1) * half + k / 2;
     float4 next = valid ? *part : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    bool ok = true;
     for (int j = 0; j < count; ++j) {
         const int sub = at.sub1 - 1 - j;
         const float4 m = next;
         if (valid && j + 1 < count) next = *(part -= half);
         f2 hs = f2_fma(f2_make(m.x, m.y), h, f2_make(m.z, m.w));  // the state before these tokens
-        if (!scan_stage_wait<kSbStages - 1>(full, j, count, &abort_flag)) break;  // the others find the abort flag set
+        ok = scan_stage_wait<kSbStages - 1>(full, j, count, &abort_flag);
+        if (!ok) break;  // the others find the abort flag set
         uint8_t* mine = smem + (j % kSbStages) * sb_stage(GW) + 4 * threadIdx.x;
         // of each token: what dh is multiplied with for df_pre, dc_pre and the token before, and do g
         f2 xf[kSbSub], xc[kSbSub], fg[kSbSub], dg[kSbSub];
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(GW * 32, 16 / GW) mlgru_scan_bwd_tma_kernel(co
         }
     }
     if (threadIdx.x == 0) bulk_wait_read<0>();
-    if (p.dh0 && valid && at.seg == 0)
+    if (ok && p.dh0 && valid && at.seg == 0)
         *reinterpret_cast<float2*>(p.dh0 + static_cast<int64_t>(at.b) * p.D + k) = f2_get(dh);
 }
 

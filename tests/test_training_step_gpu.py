@@ -122,7 +122,9 @@ def test_embed_infinities_stay_in_their_rows():
 SCAN_SHAPES = [(1, 1, 2), (1, 1, 2560), (2, 37, 128), (3, 100, 66), (1, 37, 1022), (2, 5, 64), (3, 8, 62), (1, 300, 200),
                (2, 16, 4104), (2, 129, 512), (5, 70, 34), (1, 1000, 72), (2, 2048, 8), (1, 4099, 24), (70, 3, 6),
                # 64 tokens and one more; short sequences of more channels than one launch of single warps holds
-               (1, 64, 96), (1, 65, 96), (2400, 5, 6), (2400, 9, 64), (600, 64, 264)]
+               (1, 64, 96), (1, 65, 96), (2400, 5, 6), (2400, 9, 64), (600, 64, 264),
+               # enough segments for both walks in one launch, at each width of its CTAs
+               (41, 1003, 256), (30, 1001, 264), (75, 1027, 72), (160, 968, 64)]
 
 
 @pytest.mark.parametrize("B,T,D", SCAN_SHAPES)
@@ -540,3 +542,64 @@ def test_training_steps_of_a_token_mixer():
         assert torch.equal(table_bf16, table.to(torch.bfloat16))
         before = x
     assert not torch.equal(before, mmf.embed_fwd(ids, table_bf16, scale=8.0))
+
+
+def test_two_calls_at_once_and_stream_handles():
+    """Calls that overlap on two streams, each with its own buffers, and streams given as handles, 0 among them."""
+    rng = np.random.default_rng(13)
+    ids = [torch.from_numpy(make_ids(rng, 5000, 3000, "mixed")).to(DEV) for _ in range(2)]
+    dx = [bf(rng.standard_normal((5000, 512))).to(DEV) for _ in range(2)]
+    scan = [[bf(rng.standard_normal((4, 700, 512))).to(DEV) for _ in range(4)] for _ in range(2)]
+    table = torch.randn(3000, 512, device=DEV)
+    want = [(mmf.embed_bwd(i, d, 3000), mmf.mlgru_scan_bwd(*s), mmf.embed_fwd(i, table)) for i, d, s in zip(ids, dx, scan)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [None, None]
+        for k, s in enumerate(streams):
+            got[k] = (mmf.embed_bwd(ids[k], dx[k], 3000, stream=s), mmf.mlgru_scan_bwd(*scan[k], stream=s),
+                      mmf.embed_fwd(ids[k], table, stream=s))
+        torch.cuda.synchronize()
+        for (e, r, x), (we, wr, wx) in zip(got, want):
+            assert torch.equal(e, we) and torch.equal(x, wx) and all(torch.equal(a, b) for a, b in zip(r, wr))
+    x = mmf.embed_fwd(ids[0], table, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(x, want[0][2])
+
+
+def test_given_buffers():
+    """Outputs and workspaces of the caller's; a short workspace and wrong shapes are refused."""
+    rng = np.random.default_rng(14)
+    t = [bf(rng.standard_normal((2, 200, 64))).to(DEV) for _ in range(4)]
+    want = mmf.mlgru_scan_bwd(*t)
+    outs = [torch.empty_like(t[0]) for _ in range(3)]
+    dh0 = torch.empty(2, 64, device=DEV)
+    ws = torch.empty(mmf.mlgru_scan_bwd_workspace_bytes(2, 200, 64), dtype=torch.uint8, device=DEV)
+    got = mmf.mlgru_scan_bwd(*t, outs=outs, dh0=dh0, workspace=ws)
+    assert got[3] is dh0 and all(a is b for a, b in zip(got, outs))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with pytest.raises(ValueError, match="workspace"):
+        mmf.mlgru_scan_bwd(*t, workspace=ws[:-256])
+    with pytest.raises(ValueError):
+        mmf.mlgru_scan_bwd(t[0], t[1], t[2], t[3][:, :-1])
+    with pytest.raises(ValueError):
+        mmf.mlgru_scan_bwd(*t, h0=torch.zeros(2, 63, device=DEV))
+    with pytest.raises(TypeError):
+        mmf.mlgru_scan_bwd(*t[:3], t[3].float())
+    ids = torch.from_numpy(make_ids(rng, 2000, 50, "mixed")).to(DEV)
+    dx = bf(rng.standard_normal((2000, 64))).to(DEV)
+    ws = torch.empty(mmf.embed_bwd_workspace_bytes(50, 2000, 64), dtype=torch.uint8, device=DEV)
+    assert torch.equal(mmf.embed_bwd(ids, dx, 50, workspace=ws), mmf.embed_bwd(ids, dx, 50))
+    with pytest.raises(ValueError, match="workspace"):
+        mmf.embed_bwd(ids, dx, 50, workspace=ws[:-256])
+    with pytest.raises(ValueError, match="out"):
+        mmf.embed_bwd(ids, dx, 50, accumulate=True)
+    with pytest.raises(ValueError):
+        mmf.embed_bwd(ids, dx[:-1], 50)
+    with pytest.raises(ValueError):
+        mmf.embed_bwd(ids, dx, 50, out=torch.zeros(51, 64, device=DEV))
+    with pytest.raises(mmf.MMFError):
+        mmf.embed_fwd(ids[1:], torch.zeros(50, 64, device=DEV))     # not on 16 bytes
+    two_d = ids.view(40, 50)
+    assert mmf.embed_fwd(two_d, torch.zeros(50, 64, device=DEV)).shape == (40, 50, 64)
+    assert torch.equal(mmf.embed_bwd(two_d, dx.view(40, 50, 64), 50), mmf.embed_bwd(ids, dx, 50))
