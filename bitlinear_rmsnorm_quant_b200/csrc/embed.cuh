@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const Id* __re
 }
 
 // ---------------------------------------------------------------------------
-// Rows of dtable that no token names.  The first counting launch marks the
+// Rows of dtable that no token names.  The first placing launch marks the
 // others in used[]; the launches behind it have CTAs of their own that write
 // zeros to a share of the unmarked rows, so that the writes (most of the work
 // of a small batch and a large table) run beside the sort and the sums.  A
@@ -142,7 +142,7 @@ struct SortParams {
     int per;                // places per CTA, a multiple of kSortThreads
     int ctas;
     int shift, mask;        // digit = (key >> shift) & mask
-    uint8_t* used;          // first pass, may be null: marks the rows that tokens name
+    uint8_t* used;          // first pass, may be null: the rows that tokens name, cleared while counting, marked while placing
 };
 
 template <typename Id, bool FIRST>
@@ -167,17 +167,13 @@ __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const SortPar
     for (int i = begin + threadIdx.x; i < end; i += kSortThreads) {
         const uint32_t key = sort_key<Id, FIRST>(p, i);
         atomicAdd(&bins[(key >> p.shift) & p.mask], 1);
-        if (FIRST && p.used && key < p.V) p.used[key] = 1;
     }
+    if (FIRST && p.used)  // for the placing launch to mark (the buffer is whole 16-byte words)
+        for (int64_t i = 16 * (static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x); i < p.V;
+             i += int64_t(16) * kSortThreads * p.ctas)
+            *reinterpret_cast<uint4*>(p.used + i) = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     if (threadIdx.x < kSortBins) p.count[blockIdx.x * kSortBins + threadIdx.x] = bins[threadIdx.x];
-}
-
-// used[] before the first counting launch marks it
-__global__ void __launch_bounds__(kSortThreads) embed_clear_kernel(uint8_t* used, int64_t bytes) {
-    pdl_launch_dependents();
-    const int64_t i = 16 * (static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x);
-    if (i < bytes) *reinterpret_cast<uint4*>(used + i) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 template <typename Id, bool FIRST>
@@ -265,6 +261,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(const SortPar
             const int to = base[digit] + wcount[warp][digit] + __popc(peers & ((1u << lane) - 1));
             p.key_out[to] = key;
             p.pos_out[to] = pos;
+            if (FIRST && p.used && key < p.V) p.used[key] = 1;
         }
         const int i = round + kSortThreads + t;
         if (i < end) {

@@ -628,13 +628,13 @@ ZeroParams zero_share(ZeroParams* z, int64_t bytes) {
     return share;
 }
 
-// Sorts the places by id; the launches after the first also zero shares of the
-// rows that no token names, about what they write while the sort runs, and z is
-// left with the rest.  `used` is null where nothing is to be zeroed.
+// Sorts the places by id; the launches after the first pass also zero shares of
+// the rows that no token names, about what they write while the sort runs, and
+// z is left with the rest.  `used` is null where nothing is to be zeroed.
 template <typename Id>
 mmf_status embed_sort(const void* ids, int64_t V, int64_t M, const EmbedPlan& pl, const EmbedWorkspace& w,
                       uint8_t* used, ZeroParams* z, cudaStream_t s) {
-    const int64_t share_bytes = (int64_t(24) << 20) + 256 * M;
+    const int64_t share_bytes = (int64_t(32) << 20) + 256 * M;
     for (int i = 0; i < pl.passes; ++i) {
         SortParams p{};
         p.ids = ids;
@@ -653,10 +653,10 @@ mmf_status embed_sort(const void* ids, int64_t V, int64_t M, const EmbedPlan& pl
         const dim3 block(kSortThreads);
         ZeroParams share = zero_share(z, i == 0 ? 0 : share_bytes);
         dim3 grid(static_cast<unsigned>(pl.sort_ctas + embed_zero_ctas(share, kSortThreads)));
-        mmf_status st = i == 0 ? launch(embed_count_kernel<Id, true>, grid, block, 0, s, used != nullptr, p, share)
+        mmf_status st = i == 0 ? launch(embed_count_kernel<Id, true>, grid, block, 0, s, false, p, share)
                                : launch(embed_count_kernel<Id, false>, grid, block, 0, s, true, p, share);
         if (st != MMF_OK) return st;
-        share = zero_share(z, share_bytes);
+        share = zero_share(z, i == 0 ? 0 : share_bytes);
         grid = dim3(static_cast<unsigned>(pl.sort_ctas + embed_zero_ctas(share, kSortThreads)));
         st = i == 0 ? launch(embed_place_kernel<Id, true>, grid, block, 0, s, true, p, share)
                     : launch(embed_place_kernel<Id, false>, grid, block, 0, s, true, p, share);
@@ -1255,13 +1255,7 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, i
     z.dtable = dtable;
     z.used = w.used;
     z.K = static_cast<int>(K);
-    if (!accumulate) {
-        z.end = static_cast<int>(V);
-        const int64_t per_cta = 16 * kSortThreads;
-        if ((st = launch(embed_clear_kernel, dim3(static_cast<unsigned>((V + per_cta - 1) / per_cta)), dim3(kSortThreads),
-                         0, s, false, w.used, V)) != MMF_OK)
-            return st;
-    }
+    if (!accumulate) z.end = static_cast<int>(V);
     uint8_t* used = accumulate ? nullptr : w.used;
     st = wide ? embed_sort<int64_t>(ids, V, M, pl, w, used, &z, s) : embed_sort<int32_t>(ids, V, M, pl, w, used, &z, s);
     if (st != MMF_OK) return st;
