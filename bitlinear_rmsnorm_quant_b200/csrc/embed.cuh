@@ -147,7 +147,7 @@ struct SortParams {
 
 template <typename Id, bool FIRST>
 __device__ __forceinline__ uint32_t sort_key(const SortParams& p, int i) {
-    if (!FIRST) return p.key_in[i];
+    if (!FIRST) return __ldcg(p.key_in + i);
     const int64_t id = embed_id(static_cast<const Id*>(p.ids), i, p.V);
     return static_cast<uint32_t>(id < 0 ? p.V : id);
 }
@@ -176,13 +176,82 @@ __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const SortPar
     if (threadIdx.x < kSortBins) p.count[blockIdx.x * kSortBins + threadIdx.x] = bins[threadIdx.x];
 }
 
+// What placing works with in shared memory.
+struct SortShared {
+    int base[kSortBins];                 // where the CTA's next place with a digit goes
+    int wcount[kSortWarps][kSortBins];   // a round's digits per warp, then the places before each warp's
+    int wsum[kSortBins / 32];
+};
+
+// base[] from each digit's places in all CTAs and in those before this one
+// (thread t's digit t): those of the smaller digits come first.
+__device__ __forceinline__ void sort_base(SortShared& sh, int all, int before) {
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    int v = all;
+    if (t < kSortBins) {  // inclusive sum over the digits: 8 warps of 32, then the warps before
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (lane == 31) sh.wsum[warp] = v;
+    }
+    __syncthreads();
+    if (t < kSortBins) {
+        for (int w = 0; w < warp; ++w) v += sh.wsum[w];
+        sh.base[t] = v - all + before;
+    }
+}
+
+// Places begin .. end - 1 behind base[], a thread each per round; key and pos
+// are this thread's of the first round.
+template <typename Id, bool FIRST>
+__device__ __forceinline__ void sort_place(const SortParams& p, SortShared& sh, int begin, int end, uint32_t key,
+                                           uint32_t pos) {
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    for (int round = begin; round < end; round += kSortThreads) {
+        const bool there = round + t < end;
+        for (int i = t; i < kSortWarps * kSortBins; i += kSortThreads) sh.wcount[0][i] = 0;
+        __syncthreads();
+        const uint32_t active = __ballot_sync(0xffffffffu, there);
+        uint32_t peers = 0;
+        const int digit = static_cast<int>((key >> p.shift) & static_cast<uint32_t>(p.mask));
+        if (there) {
+            peers = __match_any_sync(active, digit);  // the warp's lanes with the same digit
+            if ((peers & ((1u << lane) - 1)) == 0) sh.wcount[warp][digit] = __popc(peers);
+        }
+        __syncthreads();
+        int sum = 0;
+        if (t < kSortBins) {
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) {
+                const int c = sh.wcount[w][t];
+                sh.wcount[w][t] = sum;
+                sum += c;
+            }
+        }
+        __syncthreads();
+        if (there) {
+            const int to = sh.base[digit] + sh.wcount[warp][digit] + __popc(peers & ((1u << lane) - 1));
+            p.key_out[to] = key;
+            p.pos_out[to] = pos;
+            if (FIRST && p.used && key < p.V) p.used[key] = 1;
+        }
+        const int i = round + kSortThreads + t;
+        if (i < end) {
+            key = sort_key<Id, FIRST>(p, i);
+            pos = FIRST ? static_cast<uint32_t>(i) : __ldcg(p.pos_in + i);
+        }
+        __syncthreads();
+        if (t < kSortBins) sh.base[t] += sum;
+    }
+}
+
 template <typename Id, bool FIRST>
 __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(const SortParams p, const ZeroParams z) {
-    __shared__ int base[kSortBins];                  // where this CTA's next place with a digit goes
-    __shared__ int wcount[kSortWarps][kSortBins];    // a round's digits per warp, then the places before each warp's
-    __shared__ int part[2][4][kSortBins];            // a quarter of the CTAs' places: all, and before this one
-    __shared__ int wsum[kSortBins / 32];
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    __shared__ SortShared sh;
+    __shared__ int part[2][4][kSortBins];  // a quarter of the CTAs' places: all, and before this one
+    const int t = threadIdx.x;
     pdl_launch_dependents();
     pdl_wait();
     if (static_cast<int>(blockIdx.x) >= p.ctas) {
@@ -190,13 +259,12 @@ __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(const SortPar
         return;
     }
     const int begin = blockIdx.x * p.per, end = min(p.M, begin + p.per);
-    uint32_t key = 0, pos = 0;  // of this thread's place in the coming round
+    uint32_t key = 0, pos = 0;
     if (begin + t < end) {
         key = sort_key<Id, FIRST>(p, begin + t);
-        pos = FIRST ? static_cast<uint32_t>(begin + t) : p.pos_in[begin + t];
+        pos = FIRST ? static_cast<uint32_t>(begin + t) : __ldcg(p.pos_in + begin + t);
     }
     {
-        // digit d: places of all CTAs, and of the CTAs before this one, by quarters
         const int d = t & (kSortBins - 1), quarter = t / kSortBins;
         int count[kSortCtas / 4];
 #pragma unroll
@@ -214,62 +282,80 @@ __global__ void __launch_bounds__(kSortThreads) embed_place_kernel(const SortPar
         part[1][quarter][d] = before;
     }
     __syncthreads();
-    int all = 0, before = 0, v = 0;
+    int all = 0, before = 0;
     if (t < kSortBins) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             all += part[0][q][t];
             before += part[1][q][t];
         }
-        // exclusive sum of the totals over the digits: 8 warps of 32, then the warps before
-        v = all;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += u;
-        }
-        if (lane == 31) wsum[warp] = v;
     }
+    sort_base(sh, all, before);
+    sort_place<Id, FIRST>(p, sh, begin, end, key, pos);
+}
+
+// The whole sort of up to kClusterTokens places in one launch of one cluster:
+// the CTAs read one another's counts from shared memory, and the passes are
+// kept apart by cluster barriers (which also make the placed keys visible).
+// Two launches a pass cost the host 14 us at two passes, this one 3.5.
+constexpr int kSortCluster = 8;
+constexpr int kClusterTokens = 16384;
+
+struct SortPasses {
+    int passes, digit_bits;
+    uint32_t* key[2];
+    uint32_t* pos[2];
+};
+
+template <typename Id, bool FIRST>
+__device__ __forceinline__ void sort_cluster_pass(const SortParams& p, SortShared& sh, int* bins) {
+    const int t = threadIdx.x, rank = blockIdx.x;
+    if (t < kSortBins) bins[t] = 0;
     __syncthreads();
-    if (t < kSortBins) {
-        for (int w = 0; w < warp; ++w) v += wsum[w];
-        base[t] = v - all + before;
+    const int begin = min(p.M, rank * p.per), end = min(p.M, begin + p.per);
+    uint32_t key = 0, pos = 0;
+    for (int i = begin + t; i < end; i += kSortThreads) {
+        const uint32_t k = sort_key<Id, FIRST>(p, i);
+        atomicAdd(&bins[(k >> p.shift) & p.mask], 1);
+        if (i == begin + t) {
+            key = k;
+            pos = FIRST ? static_cast<uint32_t>(i) : __ldcg(p.pos_in + i);
+        }
     }
-    for (int round = begin; round < end; round += kSortThreads) {
-        const bool there = round + t < end;
-        for (int i = t; i < kSortWarps * kSortBins; i += kSortThreads) wcount[0][i] = 0;
-        __syncthreads();
-        const uint32_t active = __ballot_sync(0xffffffffu, there);
-        uint32_t peers = 0;
-        const int digit = static_cast<int>((key >> p.shift) & static_cast<uint32_t>(p.mask));
-        if (there) {
-            peers = __match_any_sync(active, digit);  // the warp's lanes with the same digit
-            if ((peers & ((1u << lane) - 1)) == 0) wcount[warp][digit] = __popc(peers);
-        }
-        __syncthreads();
-        int sum = 0;
-        if (t < kSortBins) {
+    if (FIRST && p.used)
+        for (int64_t i = 16 * (static_cast<int64_t>(rank) * kSortThreads + t); i < p.V; i += int64_t(16) * kSortThreads * kSortCluster)
+            *reinterpret_cast<uint4*>(p.used + i) = make_uint4(0u, 0u, 0u, 0u);
+    cluster_sync_all();
+    int all = 0, before = 0;
+    if (t < kSortBins) {
 #pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) {
-                const int c = wcount[w][t];
-                wcount[w][t] = sum;
-                sum += c;
-            }
+        for (int b = 0; b < kSortCluster; ++b) {
+            int c;
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(dsmem_addr(smem_u32(bins + t), b)) : "memory");
+            all += c;
+            if (b < rank) before += c;
         }
-        __syncthreads();
-        if (there) {
-            const int to = base[digit] + wcount[warp][digit] + __popc(peers & ((1u << lane) - 1));
-            p.key_out[to] = key;
-            p.pos_out[to] = pos;
-            if (FIRST && p.used && key < p.V) p.used[key] = 1;
-        }
-        const int i = round + kSortThreads + t;
-        if (i < end) {
-            key = sort_key<Id, FIRST>(p, i);
-            pos = FIRST ? static_cast<uint32_t>(i) : p.pos_in[i];
-        }
-        __syncthreads();
-        if (t < kSortBins) base[t] += sum;
+    }
+    sort_base(sh, all, before);
+    sort_place<Id, FIRST>(p, sh, begin, end, key, pos);
+    cluster_sync_all();
+}
+
+template <typename Id>
+__global__ void __launch_bounds__(kSortThreads) embed_sort_cluster_kernel(SortParams p, const SortPasses s) {
+    __shared__ SortShared sh;
+    __shared__ int bins[kSortBins];
+    pdl_launch_dependents();
+    for (int i = 0; i < s.passes; ++i) {
+        p.shift = i * s.digit_bits;
+        p.key_in = s.key[(i + 1) & 1];
+        p.pos_in = s.pos[(i + 1) & 1];
+        p.key_out = s.key[i & 1];
+        p.pos_out = s.pos[i & 1];
+        if (i == 0)
+            sort_cluster_pass<Id, true>(p, sh, bins);
+        else
+            sort_cluster_pass<Id, false>(p, sh, bins);
     }
 }
 

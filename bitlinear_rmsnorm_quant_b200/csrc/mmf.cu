@@ -634,6 +634,18 @@ ZeroParams zero_share(ZeroParams* z, int64_t bytes) {
 template <typename Id>
 mmf_status embed_sort(const void* ids, int64_t V, int64_t M, const EmbedPlan& pl, const EmbedWorkspace& w,
                       uint8_t* used, ZeroParams* z, cudaStream_t s) {
+    if (M <= kClusterTokens) {
+        SortParams p{};
+        p.ids = ids;
+        p.V = V;
+        p.M = static_cast<int>(M);
+        p.per = static_cast<int>((M + kSortCluster - 1) / kSortCluster + kSortThreads - 1) / kSortThreads * kSortThreads;
+        p.mask = (1 << pl.digit_bits) - 1;
+        p.used = used;
+        const SortPasses passes{pl.passes, pl.digit_bits, {w.key[0], w.key[1]}, {w.pos[0], w.pos[1]}};
+        return launch_clustered(embed_sort_cluster_kernel<Id>, dim3(kSortCluster), dim3(kSortThreads), 0, s, false,
+                                kSortCluster, p, passes);
+    }
     const int64_t share_bytes = (int64_t(32) << 20) + 256 * M;
     for (int i = 0; i < pl.passes; ++i) {
         SortParams p{};

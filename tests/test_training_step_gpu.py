@@ -75,6 +75,8 @@ def test_embed_fwd_int64_ids_beyond_32_bits():
     # one word for all tokens: a run over every summing CTA; more than one sorting CTA and round
     (1000, 300, 40, "one"), (9000, 70000, 64, "mixed"), (40000, 3, 16, "mixed"), (140000, 1000, 8, "mixed"),
     (140000, 20, 8, "one"),
+    # the most tokens of the one-launch sort, one more, and three passes of each sort
+    (16384, 3000, 16, "mixed"), (16385, 3000, 16, "mixed"), (8193, 1 << 17, 8, "mixed"), (17000, 1 << 17, 8, "mixed"),
     # keys of one digit, of exactly 8 and 16 bits, of three digits
     (1500, 255, 16, "mixed"), (1500, 256, 16, "mixed"), (1500, 65535, 8, "mixed"), (1500, 65536, 8, "mixed"),
     (1700, 1 << 20, 8, "mixed"), (2000, 5, 16, "outside"), (1200, (1 << 24) + 5, 8, "mixed")])
