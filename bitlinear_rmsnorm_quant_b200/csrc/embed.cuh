@@ -79,7 +79,9 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const Id* __re
 // Rows of dtable that no token names.  The first placing launch marks the
 // others in used[]; the launches behind it have CTAs of their own that write
 // zeros to a share of the unmarked rows, so that the writes (most of the work
-// of a small batch and a large table) run beside the sort and the sums.  A
+// of a small batch and a large table) run beside the sort and the sums (those
+// up to the marking, which cannot know, to all rows of a share: the sums come
+// later).  A
 // warp writes kZeroUnits pieces of a row of at most 2 KB and is done: many
 // short CTAs write 6.4 TB/s, 296 that stay 5.9 TB/s (32000 rows of 2560 fp32,
 // 12% of them marked).
@@ -89,8 +91,8 @@ constexpr int kZeroPiece = 128;  // 16-byte stores of a piece
 
 struct ZeroParams {
     float* dtable;
-    const uint8_t* used;
-    int begin, end;  // rows of this launch
+    const uint8_t* used;  // null: all rows
+    int begin, end;       // rows of this launch
     int K;
 };
 
@@ -108,7 +110,7 @@ __device__ __forceinline__ void embed_zero(const ZeroParams& z, int cta) {
         const unsigned of = (first + u) / pieces;
         const unsigned from = (first + u - of * pieces) * kZeroPiece;
         const int64_t row = z.begin + static_cast<int64_t>(of);
-        if (row >= z.end || z.used[row]) continue;
+        if (row >= z.end || (z.used && z.used[row])) continue;
         float4* to = reinterpret_cast<float4*>(z.dtable + row * z.K);
 #pragma unroll
         for (unsigned i = 0; i < kZeroPiece; i += 32)
@@ -342,10 +344,14 @@ __device__ __forceinline__ void sort_cluster_pass(const SortParams& p, SortShare
 }
 
 template <typename Id>
-__global__ void __launch_bounds__(kSortThreads) embed_sort_cluster_kernel(SortParams p, const SortPasses s) {
+__global__ void __launch_bounds__(kSortThreads) embed_sort_cluster_kernel(SortParams p, const SortPasses s, const ZeroParams z) {
     __shared__ SortShared sh;
     __shared__ int bins[kSortBins];
     pdl_launch_dependents();
+    if (blockIdx.x >= kSortCluster) {  // the clusters behind the first zero a share
+        embed_zero(z, blockIdx.x - kSortCluster);
+        return;
+    }
     for (int i = 0; i < s.passes; ++i) {
         p.shift = i * s.digit_bits;
         p.key_in = s.key[(i + 1) & 1];

@@ -620,9 +620,15 @@ EmbedWorkspace carve_embed(void* ws, const EmbedPlan& pl, int64_t V, int64_t M, 
     return w;
 }
 
-// The next `bytes` of the rows to zero, taken off z.
-ZeroParams zero_share(ZeroParams* z, int64_t bytes) {
+// The next `bytes` of the rows to zero, taken off z; all of them where it is
+// not yet known which tokens name, and then no more rows than at least are
+// named by none.
+ZeroParams zero_share(ZeroParams* z, int64_t bytes, bool all, int64_t M) {
     ZeroParams share = *z;
+    if (all) {
+        share.used = nullptr;
+        bytes = std::max<int64_t>(0, std::min(bytes, (z->end - M) * 4 * z->K));
+    }
     share.end = static_cast<int>(std::min<int64_t>(z->end, z->begin + bytes / (4 * z->K)));
     z->begin = share.end;
     return share;
@@ -643,8 +649,10 @@ mmf_status embed_sort(const void* ids, int64_t V, int64_t M, const EmbedPlan& pl
         p.mask = (1 << pl.digit_bits) - 1;
         p.used = used;
         const SortPasses passes{pl.passes, pl.digit_bits, {w.key[0], w.key[1]}, {w.pos[0], w.pos[1]}};
-        return launch_clustered(embed_sort_cluster_kernel<Id>, dim3(kSortCluster), dim3(kSortThreads), 0, s, false,
-                                kSortCluster, p, passes);
+        const ZeroParams share = zero_share(z, int64_t(64) << 20, true, M);
+        const int64_t zero = (embed_zero_ctas(share, kSortThreads) + kSortCluster - 1) / kSortCluster * kSortCluster;
+        return launch_clustered(embed_sort_cluster_kernel<Id>, dim3(static_cast<unsigned>(kSortCluster + zero)),
+                                dim3(kSortThreads), 0, s, false, kSortCluster, p, passes, share);
     }
     const int64_t share_bytes = (int64_t(32) << 20) + 256 * M;
     for (int i = 0; i < pl.passes; ++i) {
@@ -663,12 +671,12 @@ mmf_status embed_sort(const void* ids, int64_t V, int64_t M, const EmbedPlan& pl
         p.mask = (1 << pl.digit_bits) - 1;
         p.used = used;
         const dim3 block(kSortThreads);
-        ZeroParams share = zero_share(z, i == 0 ? 0 : share_bytes);
+        ZeroParams share = zero_share(z, i == 0 ? share_bytes / 2 : share_bytes, i == 0, M);
         dim3 grid(static_cast<unsigned>(pl.sort_ctas + embed_zero_ctas(share, kSortThreads)));
         mmf_status st = i == 0 ? launch(embed_count_kernel<Id, true>, grid, block, 0, s, false, p, share)
                                : launch(embed_count_kernel<Id, false>, grid, block, 0, s, true, p, share);
         if (st != MMF_OK) return st;
-        share = zero_share(z, i == 0 ? 0 : share_bytes);
+        share = zero_share(z, share_bytes, i == 0, M);
         grid = dim3(static_cast<unsigned>(pl.sort_ctas + embed_zero_ctas(share, kSortThreads)));
         st = i == 0 ? launch(embed_place_kernel<Id, true>, grid, block, 0, s, true, p, share)
                     : launch(embed_place_kernel<Id, false>, grid, block, 0, s, true, p, share);
