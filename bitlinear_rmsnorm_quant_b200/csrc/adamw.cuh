@@ -380,7 +380,7 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, const AdamStep& 
 // Brings a row of kAdamRow elements into L2, by one thread.  A CTA's later rows
 // are asked for kAdamAhead rows before they are worked on: the loads then wait
 // for L2 only, and HBM is kept busy whatever the warps do.
-constexpr int kAdamAhead = 2;
+constexpr int kAdamAhead = 1;
 
 template <bool STATE8, bool GRAD_BF16>
 __device__ __forceinline__ void adam_prefetch(const AdamTensor& t, int64_t at) {

@@ -468,40 +468,43 @@ def adamw_state(p: torch.Tensor, bits: int = 32) -> dict:
 _ADAMW_DESC = struct.Struct("<7QqfI")   # mmf_adamw_tensor
 
 
+# the checks of a step run once per tensor on the host: the names they use, looked up once
+_F32, _BF16, _E4M3, _E5M2 = torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.float8_e5m2
+_pack_adamw = _ADAMW_DESC.pack_into
+
+
 def _adamw_describe(t: AdamWTensor, index: int, buf, at: int) -> None:
     p, g, m, v, ms, vs, pb = t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.p_bf16
     n = p.numel()
     flags = 0
-    if g.dtype == torch.bfloat16:
+    if g.dtype is _BF16:
         flags = ADAMW_GRAD_BF16
-    elif g.dtype != torch.float32:
+    elif g.dtype is not _F32:
         raise TypeError(f"g must be torch.float32 or torch.bfloat16, got {g.dtype}")
-    if p.dtype != torch.float32:
+    if p.dtype is not _F32:
         raise TypeError(f"p must be torch.float32, got {p.dtype}")
-    msp = vsp = 0
-    if m.dtype == torch.float8_e4m3fn:
+    msp = vsp = pbp = 0
+    if m.dtype is _E4M3:
         flags |= ADAMW_STATE8
-        if v.dtype != torch.float8_e5m2:
+        if v.dtype is not _E5M2:
             raise TypeError(f"v must be torch.float8_e5m2 beside an 8-bit m, got {v.dtype}")
         if ms is None or vs is None:
             raise ValueError("m_scale and v_scale are missing: 8-bit moments need them")
         blocks = (-(-n // ADAMW_BLOCK),)
-        _like(ms, torch.float32, blocks, index, "m_scale")
-        _like(vs, torch.float32, blocks, index, "v_scale")
+        _like(ms, _F32, blocks, index, "m_scale")
+        _like(vs, _F32, blocks, index, "v_scale")
         msp, vsp = ms.data_ptr(), vs.data_ptr()
-    elif m.dtype != torch.float32 or v.dtype != torch.float32 or ms is not None or vs is not None:
+    elif m.dtype is not _F32 or v.dtype is not _F32 or ms is not None or vs is not None:
         raise TypeError("m and v must be torch.float32, or torch.float8_e4m3fn and torch.float8_e5m2 with their scales")
-    pbp = 0
     if pb is not None:
-        _like(pb, torch.bfloat16, p.shape, index, "p_bf16")
+        _like(pb, _BF16, p.shape, index, "p_bf16")
         pbp = pb.data_ptr()
     if not (p.get_device() == g.get_device() == m.get_device() == v.get_device() == index):
         raise ValueError(f"p, g, m and v must be on cuda:{index}, got {p.device}, {g.device}, {m.device}, {v.device}")
     if not (g.numel() == m.numel() == v.numel() == n and p.is_contiguous() and g.is_contiguous()
             and m.is_contiguous() and v.is_contiguous()):
         raise ValueError("p, g, m and v must be contiguous, with as many elements each")
-    _ADAMW_DESC.pack_into(buf, at, p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), msp, vsp, pbp, n,
-                          t.weight_decay, flags)
+    _pack_adamw(buf, at, p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), msp, vsp, pbp, n, t.weight_decay, flags)
 
 
 def _adamw_hyper(step, lr, beta1, beta2, eps, grad_scale, seed) -> AdamWHyper:
