@@ -24,19 +24,31 @@ __device__ __forceinline__ int64_t embed_id(const Id* __restrict__ ids, int64_t 
 // there.
 constexpr int kFwdItems = 4;
 
-template <typename Id, bool BF16>
+//
+// Index is what numbers the groups: 32 bits where they fit.  A thread divides
+// once and steps from group to group by kEmbedThreads' quotient and remainder
+// (a division for each held the kernel at 116 us, three instructions a cycle).
+template <typename Id, bool BF16, typename Index>
 __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const Id* __restrict__ ids,
                                                                   const void* __restrict__ table, int64_t V, int64_t M,
-                                                                  int K, float scale, uint16_t* __restrict__ x) {
+                                                                  int K, unsigned step_rows, unsigned step_cols, float scale,
+                                                                  uint16_t* __restrict__ x) {
     const unsigned lanes = static_cast<unsigned>(K) / 8;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kFwdItems * kEmbedThreads);
-    const int64_t row0 = first / lanes;
-    const unsigned rest = static_cast<unsigned>(first - row0 * lanes) + threadIdx.x;
+    const Index first = static_cast<Index>(blockIdx.x) * (kFwdItems * kEmbedThreads) + threadIdx.x;
+    const Index row0 = first / lanes;
+    int64_t m = static_cast<int64_t>(row0);
+    unsigned col[kFwdItems];
     int64_t id[kFwdItems];
     bool there[kFwdItems];
+    col[0] = static_cast<unsigned>(first - row0 * lanes);
 #pragma unroll
     for (int u = 0; u < kFwdItems; ++u) {
-        const int64_t m = row0 + (rest + u * kEmbedThreads) / lanes;
+        if (u > 0) {
+            const unsigned c = col[u - 1] + step_cols;
+            const bool over = c >= lanes;
+            col[u] = over ? c - lanes : c;
+            m += step_rows + (over ? 1 : 0);
+        }
         there[u] = m < M;
         id[u] = there[u] ? embed_id(ids, m, V) : -1;
     }
@@ -44,7 +56,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const Id* __re
 #pragma unroll
     for (int u = 0; u < kFwdItems; ++u) {
         lo[u] = hi[u] = make_uint4(0u, 0u, 0u, 0u);
-        const unsigned c = (rest + u * kEmbedThreads) % lanes;
+        const unsigned c = col[u];
         if (id[u] < 0) continue;
         if (BF16) {
             lo[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(table) + id[u] * K) + c);
@@ -71,7 +83,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const Id* __re
             const __nv_bfloat162 p = __floats2bfloat162_rn(__fmul_rn(v[2 * i], scale), __fmul_rn(v[2 * i + 1], scale));
             w[i] = *reinterpret_cast<const uint32_t*>(&p);
         }
-        __stcs(reinterpret_cast<uint4*>(x) + first + threadIdx.x + u * kEmbedThreads, make_uint4(w[0], w[1], w[2], w[3]));
+        __stcs(reinterpret_cast<uint4*>(x) + first + u * kEmbedThreads, make_uint4(w[0], w[1], w[2], w[3]));
     }
 }
 

@@ -556,6 +556,15 @@ mmf_status check_embed_shape(int64_t V, int64_t M, int64_t K) {
     return MMF_OK;
 }
 
+template <typename Id, bool BF16>
+mmf_status launch_embed_fwd(const void* ids, const void* table, float scale, int64_t V, int64_t M, int64_t K, uint16_t* x,
+                            int64_t ctas, bool large, cudaStream_t s) {
+    const unsigned lanes = static_cast<unsigned>(K / 8);
+    const auto kern = large ? embed_fwd_kernel<Id, BF16, uint64_t> : embed_fwd_kernel<Id, BF16, uint32_t>;
+    return launch(kern, dim3(static_cast<unsigned>(ctas)), dim3(kEmbedThreads), 0, s, false, static_cast<const Id*>(ids),
+                  table, V, M, static_cast<int>(K), kEmbedThreads / lanes, kEmbedThreads % lanes, scale, x);
+}
+
 // How the embedding gradient splits M places: over the sorting CTAs (a
 // multiple of kSortThreads each) and over the summing CTAs; and its columns.
 struct EmbedPlan {
@@ -1226,16 +1235,13 @@ int mmf_embed_fwd(const void* ids, const void* table, float scale, int64_t V, in
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t ctas = (M * (K / 8) + kFwdItems * kEmbedThreads - 1) / (kFwdItems * kEmbedThreads);
     if (ctas > kMaxDim) return MMF_ERR_UNSUPPORTED_SHAPE;
-    const dim3 grid(static_cast<unsigned>(ctas)), block(kEmbedThreads);
     const bool wide = (flags & MMF_EMBED_IDS64) != 0, bf16 = (flags & MMF_EMBED_TABLE_BF16) != 0;
-    const int k = static_cast<int>(K);
-    const int32_t* i32 = static_cast<const int32_t*>(ids);
-    const int64_t* i64 = static_cast<const int64_t*>(ids);
+    const bool large = ctas * kFwdItems * kEmbedThreads > int64_t(UINT32_MAX);
     if (wide)
-        return bf16 ? launch(embed_fwd_kernel<int64_t, true>, grid, block, 0, s, false, i64, table, V, M, k, scale, x)
-                    : launch(embed_fwd_kernel<int64_t, false>, grid, block, 0, s, false, i64, table, V, M, k, scale, x);
-    return bf16 ? launch(embed_fwd_kernel<int32_t, true>, grid, block, 0, s, false, i32, table, V, M, k, scale, x)
-                : launch(embed_fwd_kernel<int32_t, false>, grid, block, 0, s, false, i32, table, V, M, k, scale, x);
+        return bf16 ? launch_embed_fwd<int64_t, true>(ids, table, scale, V, M, K, x, ctas, large, s)
+                    : launch_embed_fwd<int64_t, false>(ids, table, scale, V, M, K, x, ctas, large, s);
+    return bf16 ? launch_embed_fwd<int32_t, true>(ids, table, scale, V, M, K, x, ctas, large, s)
+                : launch_embed_fwd<int32_t, false>(ids, table, scale, V, M, K, x, ctas, large, s);
 }
 
 size_t mmf_embed_bwd_workspace_bytes(int64_t V, int64_t M, int64_t K) {

@@ -605,3 +605,19 @@ def test_given_buffers():
     two_d = ids.view(40, 50)
     assert mmf.embed_fwd(two_d, torch.zeros(50, 64, device=DEV)).shape == (40, 50, 64)
     assert torch.equal(mmf.embed_bwd(two_d, dx.view(40, 50, 64), 50), mmf.embed_bwd(ids, dx, 50))
+
+
+def test_embed_offsets_beyond_32_bits():
+    """The most tokens a call takes, with more than 2^32 elements in x and dx."""
+    M, K, V = 65535 * 256, 264, 1000
+    g = torch.Generator(device=DEV).manual_seed(1)
+    ids = torch.randint(0, V, (M,), device=DEV, dtype=torch.int32, generator=g)
+    table = torch.randn(V, K, device=DEV, generator=g)
+    x = mmf.embed_fwd(ids, table, scale=2.0)
+    for a in (0, M // 2, M - 1000):
+        assert torch.equal(x[a:a + 1000], (table[ids[a:a + 1000].long()] * 2.0).to(torch.bfloat16))
+    d = mmf.embed_bwd(ids, x, V)
+    for v in (0, V // 2, V - 1):
+        n = int((ids == v).sum())
+        row = x[M - 1 - int((ids.flip(0) == v).int().argmax())].double()   # all of a word's rows are the same here
+        assert ((d[v].double() - n * row).abs() <= (256 + 3) * P.U * n * row.abs()).all()
