@@ -28,13 +28,12 @@ __device__ __forceinline__ int64_t embed_id(const Id* __restrict__ ids, int64_t 
 // groups per thread, kEmbedThreads apart: all of a thread's ids, then all of
 // its table reads are in flight before the first is used, and any K and M fill
 // the CTAs alike.  x is written past L2 so that the frequent words' rows stay
-// there.
+// there.  Index is what numbers the groups: 32 bits where they fit.  A thread
+// divides once and steps from group to group by kEmbedThreads' quotient and
+// remainder (131072 x 2048: 109 us; with a division for each, 116 us at three
+// instructions a cycle).
 constexpr int kFwdItems = 4;
 
-//
-// Index is what numbers the groups: 32 bits where they fit.  A thread divides
-// once and steps from group to group by kEmbedThreads' quotient and remainder
-// (a division for each held the kernel at 116 us, three instructions a cycle).
 template <typename Id, bool BF16, typename Index>
 __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const Id* __restrict__ ids,
                                                                   const void* __restrict__ table, int64_t V, int64_t M,
@@ -98,12 +97,11 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const Id* __re
 // Rows of dtable that no token names.  The first placing launch marks the
 // others in used[]; the launches behind it have CTAs of their own that write
 // zeros to a share of the unmarked rows, so that the writes (most of the work
-// of a small batch and a large table) run beside the sort and the sums (those
-// up to the marking, which cannot know, to all rows of a share: the sums come
-// later).  A
-// warp writes kZeroUnits pieces of a row of at most 2 KB and is done: many
-// short CTAs write 6.4 TB/s, 296 that stay 5.9 TB/s (32000 rows of 2560 fp32,
-// 12% of them marked).
+// of a small batch and a large table) run beside the sort and the sums.  The
+// launches up to the marking, which cannot know, zero all rows of a share: the
+// sums come later.  A warp writes kZeroUnits pieces of a row of at most 2 KB and
+// is done: many short CTAs write 6.4 TB/s, 296 that stay 5.9 TB/s (32000 rows
+// of 2560 fp32, 12% of them marked).
 // ---------------------------------------------------------------------------
 constexpr int kZeroUnits = 2;
 constexpr int kZeroPiece = 128;  // 16-byte stores of a piece

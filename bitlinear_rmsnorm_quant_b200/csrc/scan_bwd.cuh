@@ -279,10 +279,11 @@ __global__ void __launch_bounds__(kSbWarps * 32, 3) mlgru_scan_bwd_short_kernel(
 // stages in shared memory; a lane leaves df, dc and dg where it read f, c and g,
 // and they are copied out from there.  After the one barrier per kSbSub tokens
 // the first thread starts the copies out of this stage and, once those of the
-// stage before have been read, the copies in for the stage after the next.  The maps are [B][T][D] bf16, so a copy stops at the sequence's end
-// (what it reads beyond is zeros, what it would write beyond is dropped).
-// Needs D % 8 == 0 (16-byte row pitch), D >= 64 and T >= kSbSub; other shapes
-// take the kernels above.
+// stage before have been read, the copies in for the stage after the next.  The
+// maps are [B][T][D] bf16, so a copy stops at the sequence's end (what it reads
+// beyond is zeros, what it would write beyond is dropped).  Needs D % 8 == 0
+// (16-byte row pitch), D >= 64 and T >= kSbSub; other shapes take the kernels
+// above.
 // ---------------------------------------------------------------------------
 constexpr int kSbStages = 3;
 constexpr int kSbMaxGw = 4;

@@ -297,7 +297,8 @@ def bitlinear_fwd_noalloc(x: torch.Tensor, gamma: torch.Tensor, packed: torch.Te
 
 # The current stream's handle of a device by its index.  torch.cuda.current_stream builds a Stream object first
 # (3.3 us a call on the host, as long as a kernel's launch; this takes 0.1 us).
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _on(index: int, stream, call):
