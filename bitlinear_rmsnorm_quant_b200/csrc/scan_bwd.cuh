@@ -497,6 +497,12 @@ __global__ void __launch_bounds__(GW * 32, 16 / GW) mlgru_scan_bwd_tma_kernel(co
         const int n = p.T - sub * kSbSub;
 #pragma unroll
         for (int i = 0; i < kSbSub; ++i) ahead(i);  // tokens past the end read zeros and are not written
+        constexpr int ahead_by = kSbStages - 1;
+        if (threadIdx.x == 0 && j + ahead_by < count) {
+            const int slot = (j + ahead_by) % kSbStages;
+            bulk_wait_read<0>();  // the copies out of this slot, a stage ago, have been read
+            scan_stage_load<GW>(maps, smem + slot * sb_stage(GW), &full[slot], at.x, sub - ahead_by, at.b);
+        }
         if (n >= kSbSub) {
 #pragma unroll
             for (int i = kSbSub - 1; i >= 0; --i) back(i);
@@ -513,12 +519,6 @@ __global__ void __launch_bounds__(GW * 32, 16 / GW) mlgru_scan_bwd_tma_kernel(co
             tma_store_3d(&maps.dc, from + sb_tile(GW), at.x, sub * kSbSub, at.b);
             tma_store_3d(&maps.dg, from + 2 * sb_tile(GW), at.x, sub * kSbSub, at.b);
             bulk_commit();
-            constexpr int ahead_by = kSbStages - 1;
-            if (j + ahead_by < count) {
-                const int slot = (j + ahead_by) % kSbStages;
-                bulk_wait_read<1>();  // the copies out of this slot, a stage ago, have been read
-                scan_stage_load<GW>(maps, smem + slot * sb_stage(GW), &full[slot], at.x, sub - ahead_by, at.b);
-            }
         }
     }
     if (threadIdx.x == 0) bulk_wait_read<0>();
