@@ -122,9 +122,9 @@ def test_embed_argument_errors(L):
 
 def test_scan_bwd_argument_errors(L):
     f = L.mmf_mlgru_scan_bwd
-    need = L.mmf_mlgru_scan_bwd_workspace_bytes(1, 400, 64)
+    need = L.mmf_mlgru_scan_bwd_workspace_bytes(1, 4000, 64)
     assert need > 0 and L.mmf_mlgru_scan_bwd_workspace_bytes(1, 0, 64) == 0
-    ok = [A, A, A, A, None, None, 1, 400, 64, A, A, A, None, A, need, None]
+    ok = [A, A, A, A, None, None, 1, 4000, 64, A, A, A, None, A, need, None]
 
     def but(**at):
         a = list(ok)

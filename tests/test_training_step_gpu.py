@@ -121,7 +121,7 @@ def test_embed_infinities_stay_in_their_rows():
 
 # -- gradient of the recurrence ----------------------------------------------------
 
-SCAN_SHAPES = [(1, 1, 2), (1, 1, 2560), (2, 37, 128), (3, 100, 66), (1, 37, 1022), (2, 5, 64), (3, 8, 62), (1, 300, 200),
+SCAN_SHAPES = [(1, 2048, 64), (2, 2049, 72), (3, 130, 640), (1, 2600, 264), (2, 3000, 192), (1, 8200, 64), (1, 1, 2), (1, 1, 2560), (2, 37, 128), (3, 100, 66), (1, 37, 1022), (2, 5, 64), (3, 8, 62), (1, 300, 200),
                (2, 16, 4104), (2, 129, 512), (5, 70, 34), (1, 1000, 72), (2, 2048, 8), (1, 4099, 24), (70, 3, 6),
                # 64 tokens and one more; short sequences of more channels than one launch of single warps holds
                (1, 64, 96), (1, 65, 96), (2400, 5, 6), (2400, 9, 64), (600, 64, 264),
@@ -572,11 +572,11 @@ def test_two_calls_at_once_and_stream_handles():
 def test_given_buffers():
     """Outputs and workspaces of the caller's; a short workspace and wrong shapes are refused."""
     rng = np.random.default_rng(14)
-    t = [bf(rng.standard_normal((2, 200, 64))).to(DEV) for _ in range(4)]
+    t = [bf(rng.standard_normal((2, 2500, 64))).to(DEV) for _ in range(4)]
     want = mmf.mlgru_scan_bwd(*t)
     outs = [torch.empty_like(t[0]) for _ in range(3)]
     dh0 = torch.empty(2, 64, device=DEV)
-    ws = torch.empty(mmf.mlgru_scan_bwd_workspace_bytes(2, 200, 64), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(mmf.mlgru_scan_bwd_workspace_bytes(2, 2500, 64), dtype=torch.uint8, device=DEV)
     got = mmf.mlgru_scan_bwd(*t, outs=outs, dh0=dh0, workspace=ws)
     assert got[3] is dh0 and all(a is b for a, b in zip(got, outs))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
