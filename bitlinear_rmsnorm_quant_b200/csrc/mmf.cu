@@ -575,6 +575,8 @@ struct EmbedPlan {
     int threads, col_tiles;  // 8 columns per thread
 };
 
+constexpr int64_t kSumFew = 4096, kSumSome = 16384, kSumMore = 32768, kSumMany = 1 << 20;
+
 EmbedPlan embed_plan(int64_t V, int64_t M, int64_t K) {
     EmbedPlan pl{};
     const int lanes = static_cast<int>(K / 8);
@@ -585,7 +587,10 @@ EmbedPlan embed_plan(int64_t V, int64_t M, int64_t K) {
     const int64_t per = (M + kSortCtas - 1) / kSortCtas;
     pl.sort_per = static_cast<int>((per + kSortThreads - 1) / kSortThreads * kSortThreads);
     pl.sort_ctas = static_cast<int>((M + pl.sort_per - 1) / pl.sort_per);
-    pl.sum_per = M <= 32768 ? 32 : M <= (1 << 20) ? 64 : kSumMaxPer;
+    // few places per CTA where few tokens would leave SMs idle (3000 tokens of 1000
+    // columns: 31 us a call with 32 places, 25 with 16, 23 with 8), more where the
+    // longer runs' parts would cost more than the finer split gives
+    pl.sum_per = M <= kSumFew ? 8 : M <= kSumSome ? 16 : M <= kSumMore ? 32 : M <= kSumMany ? 64 : kSumMaxPer;
     pl.sum_ctas = static_cast<int>((M + pl.sum_per - 1) / pl.sum_per);
     int bits = 0;  // of the keys 0 .. V
     while ((V >> bits) != 0) ++bits;
@@ -711,6 +716,8 @@ struct ScanBwdPlan {
     int gw, groups, subs, subs_per_seg, segments;
 };
 
+constexpr int kSbMaxWaves = 4;
+
 ScanBwdPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D) {
     ScanBwdPlan pl{};
     const int64_t tiles = (D + 63) / 64;
@@ -734,7 +741,7 @@ ScanBwdPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D) {
     pl.subs = static_cast<int>((T + kSbSub - 1) / kSbSub);
     const int64_t slots = int64_t(148) * 16 / pl.gw, units = B * pl.groups;
     double best = 0.0;
-    for (int waves = 1; waves <= 4; ++waves) {
+    for (int waves = 1; waves <= kSbMaxWaves; ++waves) {
         const int64_t s = std::max<int64_t>(1, std::min<int64_t>(waves * slots / units, pl.subs));
         const int per = static_cast<int>((pl.subs + s - 1) / s);
         const int segments = (pl.subs + per - 1) / per;
@@ -1246,7 +1253,11 @@ int mmf_embed_fwd(const void* ids, const void* table, float scale, int64_t V, in
 
 size_t mmf_embed_bwd_workspace_bytes(int64_t V, int64_t M, int64_t K) {
     if (check_embed_shape(V, M, K) != MMF_OK || V == 0) return 0;
-    return carve_embed(nullptr, embed_plan(V, M, K), V, M, K).bytes;
+    // also what fewer tokens take, whose finer split leaves more parts
+    size_t bytes = carve_embed(nullptr, embed_plan(V, M, K), V, M, K).bytes;
+    for (const int64_t m : {kSumFew, kSumSome, kSumMore, kSumMany})
+        if (m < M) bytes = std::max(bytes, carve_embed(nullptr, embed_plan(V, m, K), V, m, K).bytes);
+    return bytes;
 }
 
 int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, int64_t M, int64_t K, float* dtable,
@@ -1260,7 +1271,8 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, i
     if (!aligned16(ids) || !aligned16(dx) || !aligned16(dtable) || !aligned16(workspace)) return MMF_ERR_MISALIGNED;
     const EmbedPlan pl = embed_plan(V, M, K);
     const EmbedWorkspace w = carve_embed(workspace, pl, V, M, K);
-    if (w.bytes > 0 && (!workspace || workspace_bytes < w.bytes)) return MMF_ERR_WORKSPACE;
+    const size_t need = mmf_embed_bwd_workspace_bytes(V, M, K);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return MMF_ERR_WORKSPACE;
     DeviceState* dev;
     if ((st = device_state(&dev)) != MMF_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1309,7 +1321,15 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, i
 
 size_t mmf_mlgru_scan_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D) {
     if (check_scan_shape(B, T, D) != MMF_OK || B == 0 || T == 0 || D == 0) return 0;
-    return carve_scan_bwd(nullptr, scan_bwd_plan(B, T, D), B, D).bytes;
+    // room for as many segments as scan_bwd_plan can choose, so that shorter or fewer
+    // sequences, which it may split finer, never need more
+    const ScanBwdPlan pl = scan_bwd_plan(B, T, D);
+    if (pl.one_launch) return 0;
+    const int64_t most = kSbMaxWaves * (int64_t(148) * 16 / pl.gw) / pl.groups;
+    const size_t pairs = static_cast<size_t>(D) / 2;
+    const size_t segments = static_cast<size_t>(std::max(B, std::min(B * pl.subs, most)));
+    return align256(pairs * static_cast<size_t>(B) * pl.subs * sizeof(float4)) +
+           align256(pairs * segments * sizeof(float4)) + align256(pairs * segments * sizeof(float2));
 }
 
 int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre, const uint16_t* g_pre, const uint16_t* d_o,

@@ -249,8 +249,8 @@ int mmf_embed_fwd(const void* ids, const void* table, float scale, int64_t V,
  * grouping: the same ids and dx give the same bits on every run.  A place whose
  * id is outside [0, V) takes no part.
  * ids as above; dx: bf16 [M][K] (as from mmf_bitlinear_bwd); dtable: fp32
- * [V][K].  workspace: at least mmf_embed_bwd_workspace_bytes(V, M, K) bytes,
- * no initialisation needed.  M == 0 without the flag writes zeros.
+ * [V][K].  workspace: at least mmf_embed_bwd_workspace_bytes(V, M, K) bytes, no
+ * initialisation needed; fewer tokens never need more.  M == 0 without the flag writes zeros.
  */
 size_t mmf_embed_bwd_workspace_bytes(int64_t V, int64_t M, int64_t K);
 int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V,
@@ -271,7 +271,8 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V,
  * (may be NULL: not wanted): fp32 [B][D].  Sizes as mmf_mlgru_scan.  The
  * outputs must not overlap the inputs or one another.  T = 0 copies dh_last
  * (or zeros) to dh0.  workspace: at least
- * mmf_mlgru_scan_bwd_workspace_bytes(B, T, D) bytes, no initialisation needed.
+ * mmf_mlgru_scan_bwd_workspace_bytes(B, T, D) bytes, no initialisation needed;
+ * fewer or shorter sequences never need more.
  */
 size_t mmf_mlgru_scan_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D);
 int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre,

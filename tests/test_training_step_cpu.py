@@ -120,6 +120,24 @@ def test_embed_argument_errors(L):
         assert g(None, None, 1.0, 100, 0, 64, A, None, 0, 0, None) == 7  # no tokens: zeros, on a device
 
 
+def test_workspace_of_the_largest_batch_serves_all(L):
+    """A workspace made for the most tokens is enough for any fewer of them."""
+    for V, K in ((50, 8), (32000, 2048), (100, 65536)):
+        marks = [0, 1, 1023, 1024, 1025, 3999]
+        for edge in (4096, 16384, 32768, 1 << 20):
+            marks += [edge - 1, edge, edge + 1, edge + edge // 2]
+        sizes = [L.mmf_embed_bwd_workspace_bytes(V, M, K) for M in marks]
+        assert sizes == sorted(sizes) and sizes[3] == 0 < sizes[4]
+    batches = (1, 2, 3, 4, 5, 7, 8, 16, 31, 64, 300, 1000)
+    for D in (2, 64, 1022, 2048):
+        for T in (1, 7, 8, 63, 64, 65, 1000, 4097):
+            sizes = [L.mmf_mlgru_scan_bwd_workspace_bytes(B, T, D) for B in batches]
+            assert sizes == sorted(sizes), (D, T)
+        for B in batches:
+            sizes = [L.mmf_mlgru_scan_bwd_workspace_bytes(B, T, D) for T in [*range(1, 300), 512, 1000, 2047, 2048, 9001]]
+            assert sizes == sorted(sizes), (D, B)
+
+
 def test_scan_bwd_argument_errors(L):
     f = L.mmf_mlgru_scan_bwd
     need = L.mmf_mlgru_scan_bwd_workspace_bytes(1, 4000, 64)
