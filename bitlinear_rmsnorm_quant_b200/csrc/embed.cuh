@@ -505,77 +505,146 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const SumParam
     }
 }
 
-// Joins the parts of the long runs, a CTA for each summing CTA that one begins
-// in (the others leave at once).  The parts were written up to a whole summing
-// launch ago and are read from HBM behind its last writes, so only those of the
-// run are: first which of the next kJoinBatch CTAs' first places are in it.
-constexpr int kJoinBatch = 8;
+// Joins the parts of the long runs in fp64, a warp for each summing CTA that one
+// begins in (the others have nothing to do) and for 256 columns.  The parts were
+// written up to a whole summing launch ago and are read from HBM behind its last
+// writes, so only those of the run are, and how many they are comes first.  A run
+// of more than kJoinAlone parts, as of a padding id, is divided among the CTA's
+// warps, and their sums are added in order (131072 tokens of 2048 columns, half
+// of them of one id: 212 us a call added, 518 when one warp's columns read all
+// parts in turn).  Eight parts in flight take 118 registers and 19 us instead of
+// 16 where no run is that long.
+constexpr int kJoinBatch = 4;  // parts in flight per warp
+constexpr int kJoinAlone = 16;
+constexpr int kJoinWarps = 8;
+constexpr int kJoinColumns = 256;
+static_assert(kJoinAlone >= kJoinWarps, "at most one divided run begins in the places of a CTA");
 
-__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const SumParams p) {
-    pdl_wait();
-    const uint32_t run = p.crossing[blockIdx.x];
-    const int k = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
-    if (run == kNoRun || k >= p.K) return;
-    double a[8];
-    {
-        const float4* tail = reinterpret_cast<const float4*>(p.tail + static_cast<int64_t>(blockIdx.x) * p.K + k);
-        const float4 lo = tail[0], hi = tail[1];
-        a[0] = lo.x, a[1] = lo.y, a[2] = lo.z, a[3] = lo.w;
-        a[4] = hi.x, a[5] = hi.y, a[6] = hi.z, a[7] = hi.w;
+// How many CTAs from `first` on begin in the run; sorted, so they are the first ones.
+__device__ __forceinline__ int embed_run_parts(const SumParams& p, int first, uint32_t run) {
+    const int lane = threadIdx.x & 31;
+    const auto matches = [&](int64_t b, int end) {
+        return __popc(__ballot_sync(0xffffffffu, b < end && p.key[b * p.per] == run));
+    };
+    int n = matches(first + lane, p.ctas);
+    if (n < 32) return n;
+    int lo = first + 32, hi = p.ctas;
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        n = matches(lo + static_cast<int64_t>(lane) * step, hi);
+        if (n == 0) break;
+        hi = static_cast<int>(min(static_cast<int64_t>(hi), lo + static_cast<int64_t>(n) * step));
+        lo += (n - 1) * step + 1;
     }
-    int parts = kJoinBatch;
-    for (int b = blockIdx.x + 1; parts == kJoinBatch; b += kJoinBatch) {
-        parts = 0;
-#pragma unroll
-        for (int i = 0; i < kJoinBatch; ++i)
-            if (b + i < p.ctas && p.key[static_cast<int64_t>(b + i) * p.per] == run) ++parts;  // sorted: the first ones
+    return lo - first;
+}
+
+__device__ __forceinline__ void embed_add_parts(double (&a)[8], const SumParams& p, int from, int to, int k) {
+    for (int b = from; b < to; b += kJoinBatch) {
         float4 part[kJoinBatch][2];
 #pragma unroll
         for (int i = 0; i < kJoinBatch; ++i) {
-            if (i >= parts) continue;
+            if (b + i >= to) continue;
             const float4* head = reinterpret_cast<const float4*>(p.head + static_cast<int64_t>(b + i) * p.K + k);
             part[i][0] = head[0];
             part[i][1] = head[1];
         }
 #pragma unroll
         for (int i = 0; i < kJoinBatch; ++i) {
-            if (i >= parts) continue;
+            if (b + i >= to) continue;
             a[0] += part[i][0].x, a[1] += part[i][0].y, a[2] += part[i][0].z, a[3] += part[i][0].w;
             a[4] += part[i][1].x, a[5] += part[i][1].y, a[6] += part[i][1].z, a[7] += part[i][1].w;
         }
     }
-    float s[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = static_cast<float>(a[j]);
-    embed_store8(p.dtable + static_cast<int64_t>(run) * p.K + k, s, p.scale, p.accumulate);
 }
 
+__global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const SumParams p) {
+    __shared__ double sums[kJoinWarps][kJoinColumns];  // column 8 lane + j at 32 j + lane
+    __shared__ int divided_cta, divided_parts;
+    __shared__ uint32_t divided_run;
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = blockIdx.x * kJoinWarps, cta = first + warp;
+    const int k = kJoinColumns * blockIdx.y + 8 * lane;
+    const uint32_t run = cta < p.ctas ? p.crossing[cta] : kNoRun;
+    float4 tail[2] = {};
+    if (run != kNoRun && k < p.K) {
+        const float4* from = reinterpret_cast<const float4*>(p.tail + static_cast<int64_t>(cta) * p.K + k);
+        tail[0] = from[0], tail[1] = from[1];
+    }
+    const int parts = run != kNoRun ? embed_run_parts(p, cta + 1, run) : 0;
+    const bool divided = parts > kJoinAlone;
+    if (divided && lane == 0) {
+        divided_cta = cta;
+        divided_parts = parts;
+        divided_run = run;
+    }
+    if (run != kNoRun && !divided && k < p.K) {
+        double a[8] = {tail[0].x, tail[0].y, tail[0].z, tail[0].w, tail[1].x, tail[1].y, tail[1].z, tail[1].w};
+        float s[8];
+        embed_add_parts(a, p, cta + 1, cta + 1 + parts, k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = static_cast<float>(a[j]);
+        embed_store8(p.dtable + static_cast<int64_t>(run) * p.K + k, s, p.scale, p.accumulate);
+    }
+    if (!__syncthreads_or(divided)) return;
+    const int n = divided_parts, share = (n + kJoinWarps - 1) / kJoinWarps, begin = divided_cta + 1;
+    double a[8] = {};
+    if (k < p.K) embed_add_parts(a, p, begin + min(n, warp * share), begin + min(n, (warp + 1) * share), k);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[warp][32 * j + lane] = a[j];
+    __syncthreads();
+    const int column = threadIdx.x, at = kJoinColumns * blockIdx.y + column;
+    if (at >= p.K) return;
+    double total = p.tail[static_cast<int64_t>(divided_cta) * p.K + at];
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) total += sums[i][32 * (column & 7) + (column >> 3)];
+    float* to = p.dtable + static_cast<int64_t>(divided_run) * p.K + at;
+    const float s = static_cast<float>(total) * p.scale;
+    *to = p.accumulate ? *to + s : s;
+}
+static_assert(kJoinColumns == kJoinWarps * 32);
+
 // ---------------------------------------------------------------------------
-// A few tokens: one launch, nothing sorted.  A CTA per token (and 8 columns
-// per thread) reads all ids; the first token of an id lists the others in
-// order and adds their rows, in fp32 up to 64 at a time and those in fp64; the
-// CTAs of the later ones leave at once.
+// A few tokens: one launch, nothing sorted.  A CTA per token (and up to
+// 8 kFewLanes columns) reads all ids; the first token of an id lists the others
+// in order and adds their rows, in fp32 up to 64 at a time and those in fp64; the
+// CTAs of the later ones leave at once.  A long list, as of a padding id, is
+// divided among as many slices of 8 columns a thread as fit the CTA, and their
+// sums are added in order.  1000 tokens of 2560 columns added: 14.4 us a call, 31
+// with half of the tokens of one id; 12.3 and 43 with twice the columns per CTA,
+// 20.5 and 27 with half of them.
 // ---------------------------------------------------------------------------
 constexpr int kFewTokens = 1024;
+constexpr int kFewThreads = 256;
+constexpr int kFewLanes = 128;  // of 8 columns
 constexpr int kFewGroup = 64;
-constexpr int kFewBatch = 16;  // rows of dx in flight per thread
+constexpr int kFewBatch = 8;   // rows of dx in flight per thread
+constexpr int kFewAlone = 16;  // rows that one slice adds
 
 template <typename Id>
-__global__ void __launch_bounds__(kEmbedThreads) embed_few_kernel(const Id* __restrict__ ids,
-                                                                 const uint16_t* __restrict__ dx, int64_t V, int M,
-                                                                 int K, float scale, float* __restrict__ dtable,
-                                                                 int accumulate) {
+__global__ void __launch_bounds__(kFewThreads, 4) embed_few_kernel(const Id* __restrict__ ids,
+                                                                  const uint16_t* __restrict__ dx, int64_t V, int M,
+                                                                  int K, int lanes, float scale,
+                                                                  float* __restrict__ dtable, int accumulate) {
     __shared__ int key[kFewTokens];
     __shared__ int pos[kFewTokens];
+    __shared__ double sums[8][kFewThreads];
     __shared__ int count;
     const int m = blockIdx.x;
-    for (int i = threadIdx.x; i < M; i += blockDim.x) key[i] = static_cast<int>(embed_id(ids, i, V));
+    for (int i = threadIdx.x; i < M; i += kFewThreads) key[i] = static_cast<int>(embed_id(ids, i, V));
     __syncthreads();
     const int mine = key[m];
-    bool later = mine < 0;
-    for (int i = threadIdx.x; i < m; i += blockDim.x) later |= key[i] == mine;
+    bool later = mine < 0, more = false;
+    for (int i = threadIdx.x; i < M; i += kFewThreads) {
+        later |= i < m && key[i] == mine;
+        more |= i > m && key[i] == mine;
+    }
     if (__syncthreads_or(later)) return;
-    if (threadIdx.x < 32) {
+    const bool several = __syncthreads_or(more);
+    if (!several) {
+        if (threadIdx.x == 0) pos[0] = m, count = 1;
+    } else if (threadIdx.x < 32) {
         int n = 0;
         for (int i0 = m; i0 < M; i0 += 32) {
             const int i = i0 + static_cast<int>(threadIdx.x);
@@ -587,17 +656,23 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_few_kernel(const Id* __re
         if (threadIdx.x == 0) count = n;
     }
     __syncthreads();
-    const int k = 8 * (blockIdx.y * blockDim.x + threadIdx.x);
-    if (k >= K) return;
-    double total[8] = {};
-    for (int g = 0; g < count; g += kFewGroup) {
-        const int end = min(count, g + kFewGroup);
-        float a[8] = {};
-        for (int i0 = g; i0 < end; i0 += kFewBatch) {
+    const int slices = count <= kFewAlone ? 1 : kFewThreads / lanes;
+    const int slice = threadIdx.x / lanes, share = (count + slices - 1) / slices;
+    const int k = 8 * (blockIdx.y * lanes + threadIdx.x - slice * lanes);
+    const int from = min(count, slice * share), to = slice < slices && k < K ? min(count, from + share) : from;
+    float a[8] = {};
+    if (slices > 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[j][threadIdx.x] = 0.0;
+    }
+    for (int i0 = from; i0 < to;) {
+        const int end = min(to, i0 + kFewGroup);
+        for (; i0 < end; i0 += kFewBatch) {
             uint4 row[kFewBatch];
 #pragma unroll
             for (int u = 0; u < kFewBatch; ++u)
-                if (i0 + u < end) row[u] = __ldg(reinterpret_cast<const uint4*>(dx + static_cast<int64_t>(pos[i0 + u]) * K + k));
+                if (i0 + u < end)
+                    row[u] = __ldg(reinterpret_cast<const uint4*>(dx + static_cast<int64_t>(pos[i0 + u]) * K + k));
 #pragma unroll
             for (int u = 0; u < kFewBatch; ++u) {
                 if (i0 + u >= end) break;
@@ -607,13 +682,26 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_few_kernel(const Id* __re
                 for (int j = 0; j < 8; ++j) a[j] += v[j];
             }
         }
+        if (slices > 1) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) total[j] += a[j];
+            for (int j = 0; j < 8; ++j) {
+                sums[j][threadIdx.x] += a[j];
+                a[j] = 0.0f;
+            }
+        }
     }
-    float s[8];
+    if (slices > 1) {
+        __syncthreads();
+        if (slice == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = static_cast<float>(total[j]);
-    embed_store8(dtable + static_cast<int64_t>(mine) * K + k, s, scale, accumulate);
+            for (int j = 0; j < 8; ++j) {
+                double total = 0.0;
+                for (int i = 0; i < slices; ++i) total += sums[j][i * lanes + threadIdx.x];
+                a[j] = static_cast<float>(total);
+            }
+        }
+    }
+    if (slice == 0 && k < K) embed_store8(dtable + static_cast<int64_t>(mine) * K + k, a, scale, accumulate);
 }
 
 }  // namespace mmf

@@ -580,9 +580,10 @@ constexpr int64_t kSumFew = 4096, kSumSome = 16384, kSumMore = 32768, kSumMany =
 EmbedPlan embed_plan(int64_t V, int64_t M, int64_t K) {
     EmbedPlan pl{};
     const int lanes = static_cast<int>(K / 8);
-    pl.col_tiles = (lanes + kEmbedThreads - 1) / kEmbedThreads;
-    pl.threads = ((lanes + pl.col_tiles - 1) / pl.col_tiles + 31) / 32 * 32;
     pl.few = M <= kFewTokens;
+    const int most = pl.few ? kFewLanes : kEmbedThreads;
+    pl.col_tiles = (lanes + most - 1) / most;
+    pl.threads = ((lanes + pl.col_tiles - 1) / pl.col_tiles + 31) / 32 * 32;
     if (pl.few) return pl;
     const int64_t per = (M + kSortCtas - 1) / kSortCtas;
     pl.sort_per = static_cast<int>((per + kSortThreads - 1) / kSortThreads * kSortThreads);
@@ -1284,10 +1285,10 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, i
         if (M == 0) return MMF_OK;
         const dim3 grid(static_cast<unsigned>(M), static_cast<unsigned>(pl.col_tiles));
         const int m = static_cast<int>(M), k = static_cast<int>(K), add = accumulate;
-        return wide ? launch(embed_few_kernel<int64_t>, grid, block, 0, s, false, static_cast<const int64_t*>(ids), dx,
-                             V, m, k, scale, dtable, add)
-                    : launch(embed_few_kernel<int32_t>, grid, block, 0, s, false, static_cast<const int32_t*>(ids), dx,
-                             V, m, k, scale, dtable, add);
+        return wide ? launch(embed_few_kernel<int64_t>, grid, dim3(kFewThreads), 0, s, false,
+                             static_cast<const int64_t*>(ids), dx, V, m, k, pl.threads, scale, dtable, add)
+                    : launch(embed_few_kernel<int32_t>, grid, dim3(kFewThreads), 0, s, false,
+                             static_cast<const int32_t*>(ids), dx, V, m, k, pl.threads, scale, dtable, add);
     }
     ZeroParams z{};
     z.dtable = dtable;
@@ -1316,7 +1317,9 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, i
     if ((st = launch(embed_sum_kernel, dim3(static_cast<unsigned>(pl.sum_ctas + embed_zero_ctas(z, pl.threads)), tiles),
                      block, 0, s, true, p, z)) != MMF_OK)
         return st;
-    return launch(embed_join_kernel, dim3(static_cast<unsigned>(pl.sum_ctas), tiles), block, 0, s, true, p);
+    const dim3 joins(static_cast<unsigned>((pl.sum_ctas + kJoinWarps - 1) / kJoinWarps),
+                     static_cast<unsigned>((K + kJoinColumns - 1) / kJoinColumns));
+    return launch(embed_join_kernel, joins, dim3(kJoinWarps * 32), 0, s, true, p);
 }
 
 size_t mmf_mlgru_scan_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D) {

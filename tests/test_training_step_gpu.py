@@ -100,6 +100,34 @@ def test_embed_bwd(M, V, K, kind, add):
     assert torch.equal(again, got)
 
 
+@pytest.mark.parametrize("M,V,K", [
+    # one launch: lists that one slice adds, lists divided among 2, 4 and 8 slices, with columns left over
+    (60, 40, 24), (700, 40, 1032), (1024, 500, 2064), (900, 300, 264), (512, 90, 520),
+    # runs over many summing CTAs, 256 columns and fewer or more, some behind the CTA's last join warp
+    (3000, 900, 264), (4096, 50, 1000), (4097, 50, 256), (9000, 2000, 520), (20000, 30, 248), (40000, 100, 16)])
+@pytest.mark.parametrize("frequent", ["first", "last", "two"])
+def test_embed_bwd_of_frequent_ids(M, V, K, frequent):
+    """Padded batches: most tokens of one or two ids."""
+    rng = np.random.default_rng(M + K)
+    ids = make_ids(rng, M, V, "mixed")
+    at = rng.random(M)
+    if frequent == "two":
+        ids[at < 0.35] = V // 3
+        ids[at > 0.6] = V // 3 + 1
+    else:
+        ids[at < 0.8] = 0 if frequent == "first" else V - 1
+    dx = bf(rng.standard_normal((M, K)))
+    base = rng.standard_normal((V, K)).astype(np.float32)
+    ids_d, dx_d = torch.from_numpy(ids).to(DEV), dx.to(DEV)
+    for add in (False, True):
+        want, bound = P.embed_bwd(ids, f64(dx), V, 0.5, base if add else None)
+        outs = [torch.from_numpy(base).to(DEV) for _ in range(2)]
+        for out in outs:
+            mmf.embed_bwd(ids_d, dx_d, V, scale=0.5, out=out, accumulate=add)
+        assert (np.abs(f64(outs[0]) - want) <= bound).all()
+        assert torch.equal(*outs)
+
+
 def test_embed_bwd_empty():
     d = mmf.embed_bwd(torch.zeros(0, dtype=torch.int64, device=DEV), torch.zeros(0, 16, dtype=torch.bfloat16, device=DEV),
                       5, out=torch.ones(5, 16, device=DEV))
