@@ -718,28 +718,32 @@ struct ScanBwdPlan {
 };
 
 constexpr int kSbMaxWaves = 4;
+constexpr int64_t kSbShortSteps = 4096;
 
 ScanBwdPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D) {
     ScanBwdPlan pl{};
     const int64_t tiles = (D + 63) / 64;
-    // where one wave of single warps holds the channels of all (short) sequences,
-    // a second launch costs more than it splits (37 tokens of 1022 channels: 22.8 us
-    // a call with two launches, 17.5 with one)
-    pl.one_launch = T <= kSbShort && B * tiles <= int64_t(148) * 16;
+    pl.subs = static_cast<int>((T + kSbSub - 1) / kSbSub);
+    // short sequences in one launch, as long as their walk there and back takes no
+    // longer than a second launch and the split (16 tokens of 2048 channels: 11.5 us
+    // a call against 14.7; 48 tokens 16.4 against 14.7), and as long as one wave of
+    // warps is enough (64 sequences of 16 tokens 14.4 us against 14.6, of 24 tokens
+    // 18.5 against 16.4); a single step, which tensor copies do not take, always
+    // (512 sequences of a token of 2560 channels: 22.6 us against 32.8)
+    pl.one_launch = T < kSbSub || (T <= kSbShort && B * tiles * pl.subs <= kSbShortSteps);
     if (pl.one_launch) {
         pl.groups = static_cast<int>(tiles);
-        pl.subs = pl.subs_per_seg = static_cast<int>((T + kSbSub - 1) / kSbSub);
+        pl.subs_per_seg = pl.subs;
         pl.segments = 1;
         pl.gw = 1;
         return pl;
     }
-    pl.tma = D % 8 == 0 && D >= 64 && T >= kSbSub && 2 * T * D < (int64_t(1) << 40);
+    pl.tma = D % 8 == 0 && D >= 64 && 2 * T * D < (int64_t(1) << 40);
     pl.gw = 1;
     if (pl.tma)  // the widest CTA that wastes no more than a quarter of its channels
         for (int gw = 2; gw <= kSbMaxGw; ++gw)
             if (4 * ((tiles + gw - 1) / gw * gw) <= 5 * tiles) pl.gw = gw;
     pl.groups = static_cast<int>((tiles + pl.gw - 1) / pl.gw);
-    pl.subs = static_cast<int>((T + kSbSub - 1) / kSbSub);
     const int64_t slots = int64_t(148) * 16 / pl.gw, units = B * pl.groups;
     double best = 0.0;
     for (int waves = 1; waves <= kSbMaxWaves; ++waves) {
@@ -1382,6 +1386,7 @@ int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre, const uint1
     p.subs_per_seg = pl.subs_per_seg;
     p.tiles = pl.groups;
     p.items = B * pl.segments * static_cast<int64_t>(pl.groups);
+    if (p.items > kMaxDim) return MMF_ERR_UNSUPPORTED_SHAPE;
     if (pl.tma) {
         ScanBwdMaps maps;
         const std::pair<CUtensorMap*, const void*> all[7] = {{&maps.f, f_pre},   {&maps.c, c_pre},   {&maps.g, g_pre},

@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kSbWarps * 32, 3) mlgru_scan_bwd_kernel(const 
 // Short sequences (kSbShort tokens at most) in one launch: a warp walks its 64
 // channels' tokens forward, keeping the state before every kSbSub-th in shared
 // memory, and takes them backwards from there.
-constexpr int kSbShort = 64;
+constexpr int kSbShort = 40;
 
 __global__ void __launch_bounds__(kSbWarps * 32, 3) mlgru_scan_bwd_short_kernel(const ScanBwdParams p) {
     __shared__ float2 kept[kSbWarps][kSbShort / kSbSub][32];
@@ -282,8 +282,7 @@ __global__ void __launch_bounds__(kSbWarps * 32, 3) mlgru_scan_bwd_short_kernel(
 // stage before have been read, the copies in for the stage after the next.  The
 // maps are [B][T][D] bf16, so a copy stops at the sequence's end (what it reads
 // beyond is zeros, what it would write beyond is dropped).  Needs D % 8 == 0
-// (16-byte row pitch), D >= 64 and T >= kSbSub; other shapes take the kernels
-// above.
+// (16-byte row pitch) and D >= 64; other shapes take the kernels above.
 // ---------------------------------------------------------------------------
 constexpr int kSbStages = 3;
 constexpr int kSbMaxGw = 4;

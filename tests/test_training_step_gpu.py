@@ -151,8 +151,8 @@ def test_embed_infinities_stay_in_their_rows():
 
 SCAN_SHAPES = [(1, 2048, 64), (2, 2049, 72), (3, 130, 640), (1, 2600, 264), (2, 3000, 192), (1, 8200, 64), (1, 1, 2), (1, 1, 2560), (2, 37, 128), (3, 100, 66), (1, 37, 1022), (2, 5, 64), (3, 8, 62), (1, 300, 200),
                (2, 16, 4104), (2, 129, 512), (5, 70, 34), (1, 1000, 72), (2, 2048, 8), (1, 4099, 24), (70, 3, 6),
-               # 64 tokens and one more; short sequences of more channels than one launch of single warps holds
-               (1, 64, 96), (1, 65, 96), (2400, 5, 6), (2400, 9, 64), (600, 64, 264),
+               # the most tokens of one launch, and one more; short sequences of more channels than it takes; single steps
+               (1, 40, 96), (1, 41, 96), (1, 64, 96), (1, 65, 96), (600, 7, 264), (600, 8, 264), (4100, 7, 64), (4100, 8, 64), (2400, 5, 6), (2400, 9, 64), (600, 64, 264),
                # enough segments for both walks in one launch, at each width of its CTAs
                (41, 1003, 256), (30, 1001, 264), (75, 1027, 72), (160, 968, 64)]
 
