@@ -546,6 +546,29 @@ mmf_status fwd_impl(const uint16_t* x, const float* gamma, float eps, int64_t M,
     return MMF_OK;
 }
 
+// A caller's buffer; what a call writes must not overlap anything else of it.
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uintptr_t>(b.bytes) &&
+           y < x + static_cast<uintptr_t>(a.bytes);
+}
+
+template <size_t W, size_t R>
+bool written_apart(const Span (&written)[W], const Span (&read)[R]) {
+    for (size_t i = 0; i < W; ++i) {
+        for (size_t j = i + 1; j < W; ++j)
+            if (overlap(written[i], written[j])) return false;
+        for (const Span& r : read)
+            if (overlap(written[i], r)) return false;
+    }
+    return true;
+}
+
 // ---------------------------------------------------------------------------
 // embedding
 // ---------------------------------------------------------------------------
@@ -1242,12 +1265,14 @@ int mmf_embed_fwd(const void* ids, const void* table, float scale, int64_t V, in
     if (M == 0) return MMF_OK;
     if (!ids || !x || (V > 0 && !table)) return MMF_ERR_INVALID_ARG;
     if (!aligned16(ids) || !aligned16(table) || !aligned16(x)) return MMF_ERR_MISALIGNED;
+    const bool wide = (flags & MMF_EMBED_IDS64) != 0, bf16 = (flags & MMF_EMBED_TABLE_BF16) != 0;
+    if (!written_apart({Span{x, 2 * M * K}}, {Span{ids, (wide ? 8 : 4) * M}, Span{table, (bf16 ? 2 : 4) * V * K}}))
+        return MMF_ERR_INVALID_ARG;
     DeviceState* dev;
     if ((st = device_state(&dev)) != MMF_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t ctas = (M * (K / 8) + kFwdItems * kEmbedThreads - 1) / (kFwdItems * kEmbedThreads);
     if (ctas > kMaxDim) return MMF_ERR_UNSUPPORTED_SHAPE;
-    const bool wide = (flags & MMF_EMBED_IDS64) != 0, bf16 = (flags & MMF_EMBED_TABLE_BF16) != 0;
     const bool large = ctas * kFwdItems * kEmbedThreads > int64_t(UINT32_MAX);
     if (wide)
         return bf16 ? launch_embed_fwd<int64_t, true>(ids, table, scale, V, M, K, x, ctas, large, s)
@@ -1278,6 +1303,9 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V, i
     const EmbedWorkspace w = carve_embed(workspace, pl, V, M, K);
     const size_t need = mmf_embed_bwd_workspace_bytes(V, M, K);
     if (need > 0 && (!workspace || workspace_bytes < need)) return MMF_ERR_WORKSPACE;
+    if (!written_apart({Span{dtable, 4 * V * K}, Span{workspace, static_cast<int64_t>(need)}},
+                       {Span{ids, (wide ? 8 : 4) * M}, Span{dx, 2 * M * K}}))
+        return MMF_ERR_INVALID_ARG;
     DeviceState* dev;
     if ((st = device_state(&dev)) != MMF_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1354,6 +1382,12 @@ int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre, const uint1
         return MMF_ERR_MISALIGNED;
     const size_t need = mmf_mlgru_scan_bwd_workspace_bytes(B, T, D);
     if (need > 0 && (!workspace || workspace_bytes < need)) return MMF_ERR_WORKSPACE;
+    const int64_t all = 2 * B * T * D, state = 4 * B * D;
+    if (!written_apart({Span{df_pre, all}, Span{dc_pre, all}, Span{dg_pre, all}, Span{dh0, state},
+                        Span{workspace, static_cast<int64_t>(need)}},
+                       {Span{f_pre, all}, Span{c_pre, all}, Span{g_pre, all}, Span{d_o, all}, Span{h0, state},
+                        Span{dh_last, state}}))
+        return MMF_ERR_INVALID_ARG;
     DeviceState* dev;
     if ((st = device_state(&dev)) != MMF_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -232,7 +232,7 @@ int mmf_bitlinear_bwd(const uint16_t* dy, const uint16_t* x, const float* gamma,
  * bf16 [V][K] with MMF_EMBED_TABLE_BF16; x: bf16 [M][K].  An id outside
  * [0, V) (the usual -1 of a padded place) gives a row of zeros.  K % 8 == 0,
  * 8 <= K <= 65536, V < 2^31 - 1, M as above; scale finite.  x must not overlap
- * the inputs.
+ * the inputs (refused, as for the gradients below).
  */
 #define MMF_EMBED_IDS64 1u       /* ids are int64 (else int32) */
 #define MMF_EMBED_TABLE_BF16 2u  /* mmf_embed_fwd: the table is bf16 (else fp32) */
@@ -250,7 +250,9 @@ int mmf_embed_fwd(const void* ids, const void* table, float scale, int64_t V,
  * id is outside [0, V) takes no part.
  * ids as above; dx: bf16 [M][K] (as from mmf_bitlinear_bwd); dtable: fp32
  * [V][K].  workspace: at least mmf_embed_bwd_workspace_bytes(V, M, K) bytes, no
- * initialisation needed; fewer tokens never need more.  M == 0 without the flag writes zeros.
+ * initialisation needed; fewer tokens never need more.  dtable and the workspace
+ * must not overlap the inputs or one another.  M == 0 without the flag writes
+ * zeros.
  */
 size_t mmf_embed_bwd_workspace_bytes(int64_t V, int64_t M, int64_t K);
 int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V,
@@ -269,7 +271,7 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V,
  * in fp32.  f_pre, c_pre, g_pre, d_o (the gradient of o) and the outputs
  * df_pre, dc_pre, dg_pre: bf16 [B][T][D]; h0, dh_last (may be NULL) and dh0
  * (may be NULL: not wanted): fp32 [B][D].  Sizes as mmf_mlgru_scan.  The
- * outputs must not overlap the inputs or one another.  T = 0 copies dh_last
+ * outputs and the workspace must not overlap the inputs or one another.  T = 0 copies dh_last
  * (or zeros) to dh0.  workspace: at least
  * mmf_mlgru_scan_bwd_workspace_bytes(B, T, D) bytes, no initialisation needed;
  * fewer or shorter sequences never need more.

@@ -138,6 +138,38 @@ def test_workspace_of_the_largest_batch_serves_all(L):
             assert sizes == sorted(sizes), (D, B)
 
 
+def test_overlaps_are_refused(L):
+    """Outputs over inputs, over one another or over the workspace; buffers next to one another are apart."""
+    apart = 0 if torch.cuda.is_available() else 7
+    if apart == 0:
+        pytest.skip("the addresses below are no memory")
+    at = [0x10000000 * (i + 1) for i in range(12)]
+    fwd, bwd, scan = L.mmf_embed_fwd, L.mmf_embed_bwd, L.mmf_mlgru_scan_bwd
+    ids, table, x = at[:3]
+    assert fwd(ids, table, 1.0, 100, 2000, 64, x, 0, None) == apart
+    assert fwd(ids, table, 1.0, 100, 2000, 64, table + 4 * 100 * 64, 0, None) == apart      # behind the table
+    assert fwd(ids, table, 1.0, 100, 2000, 64, table + 4 * 100 * 64 - 16, 0, None) == 1
+    assert fwd(ids, table, 1.0, 100, 2000, 64, ids + 4 * 2000 - 16, 0, None) == 1
+    assert fwd(ids, table, 1.0, 100, 2000, 64, ids + 8 * 2000 - 16, 0, None) == apart
+    assert fwd(ids, table, 1.0, 100, 2000, 64, ids + 8 * 2000 - 16, 1, None) == 1           # int64 ids are longer
+    dx, d, ws = at[1:4]
+    need = L.mmf_embed_bwd_workspace_bytes(100, 2000, 64)
+    assert bwd(ids, dx, 1.0, 100, 2000, 64, d, ws, need, 0, None) == apart
+    for d_at, ws_at in ((dx, ws), (ids, ws), (ws, ws), (ws + need - 16, ws), (d, dx + 2 * 2000 * 64 - 16), (d, ids)):
+        assert bwd(ids, dx, 1.0, 100, 2000, 64, d_at, ws_at, need, 0, None) == 1
+    assert bwd(ids, dx, 1.0, 100, 2000, 64, ws + need, ws, need, 0, None) == apart
+    need = L.mmf_mlgru_scan_bwd_workspace_bytes(2, 4000, 64)
+    ok = [*at[:6], 2, 4000, 64, *at[6:11], need, None]
+    pointers = (0, 1, 2, 3, 4, 5, 9, 10, 11, 12, 13)
+    assert scan(*ok) == apart
+    for w in (9, 10, 11, 12, 13):
+        for other in pointers:
+            if other != w:
+                a = list(ok)
+                a[w] = a[other]
+                assert scan(*a) == 1, (w, other)
+
+
 def test_scan_bwd_argument_errors(L):
     f = L.mmf_mlgru_scan_bwd
     need = L.mmf_mlgru_scan_bwd_workspace_bytes(1, 4000, 64)
