@@ -734,7 +734,10 @@ mmf_status check_scan_shape(int64_t B, int64_t T, int64_t D) {
 // copies, else of single warps) over channel groups, sequences and segments of
 // whole kSbSub-token steps.  Segments are as many as keep the time of all waves
 // of resident CTAs shortest, a CTA's time being its steps, about two steps to
-// begin and end, and 0.15 steps for each other segment whose map it folds.
+// begin and end, and 0.1 steps for each other segment whose map it folds: four
+// waves at most, and less than one where few channels would make segments of so
+// few steps that the fold takes longer than they (2048 tokens of 512 channels:
+// 14.4 us, 26.5 with a whole wave; 131072 of 64 channels: 78 and 185).
 struct ScanBwdPlan {
     bool one_launch, tma;
     int gw, groups, subs, subs_per_seg, segments;
@@ -769,13 +772,14 @@ ScanBwdPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D) {
     pl.groups = static_cast<int>((tiles + pl.gw - 1) / pl.gw);
     const int64_t slots = int64_t(148) * 16 / pl.gw, units = B * pl.groups;
     double best = 0.0;
-    for (int waves = 1; waves <= kSbMaxWaves; ++waves) {
-        const int64_t s = std::max<int64_t>(1, std::min<int64_t>(waves * slots / units, pl.subs));
+    // from four waves of CTAs down to a sixteenth of one
+    for (int parts = 16 * kSbMaxWaves; parts > 0; parts -= parts > 16 ? 16 : 1) {
+        const int64_t s = std::max<int64_t>(1, std::min<int64_t>(parts * slots / (16 * units), pl.subs));
         const int per = static_cast<int>((pl.subs + s - 1) / s);
         const int segments = (pl.subs + per - 1) / per;
         const int64_t rounds = (units * segments + slots - 1) / slots;
-        const double cost = static_cast<double>(rounds) * (per + 2.0 + 0.15 * segments);
-        if (waves == 1 || cost < best) {
+        const double cost = static_cast<double>(rounds) * (per + 2.0 + 0.1 * segments);
+        if (best == 0.0 || cost < best) {
             best = cost;
             pl.subs_per_seg = per;
             pl.segments = segments;
