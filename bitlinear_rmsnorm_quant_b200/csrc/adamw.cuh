@@ -14,7 +14,8 @@
 // moment's change of 1 - beta per step is far below an 8-bit code's step, so
 // rounding to nearest would stop it from moving; the codes are rounded up or
 // down at random with the right mean instead, by 16 bits a moment of the
-// SplitMix64 stream (seed, tensor).  The update takes the moments before they
+// SplitMix64 stream (seed, tensor); the caller's seed is another at every step,
+// or the bits would be fixed thresholds.  The update takes the moments before they
 // are rounded.  |m| below the smallest normal code becomes 0; a positive v is
 // kept at least at the smallest normal code, so it never reads as 0.
 //

@@ -509,13 +509,16 @@ def _adamw_describe(t: AdamWTensor, index: int, buf, at: int) -> None:
 
 
 def _adamw_hyper(step, lr, beta1, beta2, eps, grad_scale, seed) -> AdamWHyper:
-    return AdamWHyper(lr, beta1, beta2, eps, grad_scale, step, seed)
+    """seed None: the step.  The noise of 8-bit moments has to be new at every step; with one that stays, each
+    element rounds at a threshold of its own for good and its moments are biased (v 3 times too large in the median
+    after some hundred steps)."""
+    return AdamWHyper(lr, beta1, beta2, eps, grad_scale, step, step if seed is None else seed)
 
 
 def adamw_scalars(step: int, lr: float, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8,
-                  grad_scale: float = 1.0, seed: int = 0) -> torch.Tensor:
+                  grad_scale: float = 1.0, seed: int | None = None) -> torch.Tensor:
     """A step's scalars as 32 bytes on the host (pinned when there is a GPU): copy them into the device buffer
-    that a captured adamw_step was given as `scalars` before each replay."""
+    that a captured adamw_step was given as `scalars` before each replay.  `seed` as for adamw_step."""
     out = torch.zeros(32, dtype=torch.uint8, pin_memory=torch.cuda.is_available())
     hyper = _adamw_hyper(step, lr, beta1, beta2, eps, grad_scale, seed)
     check(lib().mmf_adamw_scalars_at(C.byref(hyper), out.data_ptr()), "mmf_adamw_scalars_at")
@@ -523,9 +526,11 @@ def adamw_scalars(step: int, lr: float, beta1: float = 0.9, beta2: float = 0.95,
 
 
 def adamw_step(tensors, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8,
-               grad_scale: float = 1.0, seed: int = 0, scalars: torch.Tensor | None = None, stream=None) -> None:
+               grad_scale: float = 1.0, seed: int | None = None, scalars: torch.Tensor | None = None, stream=None) -> None:
     """One AdamW step over a sequence of AdamWTensor, in place; `step` counts from 1.  With `scalars` (uint8[32]
-    on the device, see adamw_scalars) the kernel takes lr, the bias corrections, grad_scale and seed from there."""
+    on the device, see adamw_scalars) the kernel takes lr, the bias corrections, grad_scale and seed from there.
+    `seed` is that of the rounding noise of 8-bit moments (without any it changes nothing): the step when not given;
+    a caller that gives one gives another at every step, or the moments are biased."""
     tensors = list(tensors)
     if not tensors:
         return

@@ -309,6 +309,12 @@ int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre,
  * smallest normal code.  A block in which a moment is 2^127 or more, infinite
  * or NaN reads as NaN from then on.  All zeros are the fresh states of either
  * kind.
+ * With MMF_ADAMW_STATE8 the seed must be another at every step of a run (the
+ * step's number will do): with one that stays, an element draws the same bits
+ * each time, which is a fixed threshold to round at, and its moments are biased
+ * for good (after some hundred steps v is 3 times too large in the median, 10
+ * times once the gradients have halved).  A graph that is captured without
+ * `scalars` repeats its step's seed, and its bias corrections, on every replay.
  *
  * tensors: HOST array, read during the call only; n == 0 is skipped (its
  * pointers may be NULL).  p, p_bf16, m, v, m_scale and v_scale of one call must
@@ -343,7 +349,7 @@ typedef struct mmf_adamw_tensor {
 typedef struct mmf_adamw_hyper {
     double lr, beta1, beta2, eps, grad_scale;
     int64_t step;
-    uint64_t seed;
+    uint64_t seed;       /* MMF_ADAMW_STATE8: another at every step, as of `step` */
 } mmf_adamw_hyper;
 
 typedef struct mmf_adamw_scalars {
