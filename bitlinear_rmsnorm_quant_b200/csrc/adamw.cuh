@@ -90,8 +90,10 @@ __host__ __device__ __forceinline__ unsigned long long splitmix_mix(unsigned lon
 }
 constexpr unsigned long long kSplitmixGolden = 0x9E3779B97F4A7C15ull;
 
+// The key of a tensor's stream, from all 64 bits of the seed: of a seed below
+// 2^32 it is mix(seed 2^32 + tensor), as of the input streams, since mix(0) = 0.
 __host__ __device__ __forceinline__ unsigned long long adam_key(unsigned long long seed, unsigned long long tensor) {
-    return splitmix_mix((seed << 32) + tensor);
+    return splitmix_mix((seed << 32) + tensor + splitmix_mix(seed >> 32));
 }
 
 // two 8-bit floats -> fp32 (exact)

@@ -512,7 +512,11 @@ def _adamw_hyper(step, lr, beta1, beta2, eps, grad_scale, seed) -> AdamWHyper:
     """seed None: the step.  The noise of 8-bit moments has to be new at every step; with one that stays, each
     element rounds at a threshold of its own for good and its moments are biased (v 3 times too large in the median
     after some hundred steps)."""
-    return AdamWHyper(lr, beta1, beta2, eps, grad_scale, step, step if seed is None else seed)
+    if seed is None:
+        seed = step
+    elif not -(1 << 63) <= seed < 1 << 64:
+        raise ValueError(f"seed must fit 64 bits, got {seed}")
+    return AdamWHyper(lr, beta1, beta2, eps, grad_scale, step, seed)
 
 
 def adamw_scalars(step: int, lr: float, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8,

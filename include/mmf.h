@@ -303,7 +303,8 @@ int mmf_mlgru_scan_bwd(const uint16_t* f_pre, const uint16_t* c_pre,
  * the block's largest |m| < 2^(e+1), e taken as at least -90, m_scale =
  * 2^(e-7), and v_scale = 2^(e-14) likewise.  The codes are rounded up or down
  * at random, with the right mean: 16 bits per moment from draw floor(i / 2) of
- * the SplitMix64 stream (seed, index of the tensor in the call) for element i;
+ * the SplitMix64 stream (seed, index of the tensor in the call) for element i,
+ * all 64 bits of the seed taken;
  * p is updated with the moments before they are rounded.  |m| below the
  * smallest normal code becomes 0; a positive v is kept at least at the
  * smallest normal code.  A block in which a moment is 2^127 or more, infinite

@@ -1,8 +1,11 @@
 """8-bit moments over many steps: they follow the 32-bit ones in the mean as
 long as the rounding noise is new at every step, which it is by default."""
+import numpy as np
 import pytest
 import torch
 
+import training_plain as P
+from bitlinear_rmsnorm_quant_b200 import inputs as I
 from bitlinear_rmsnorm_quant_b200 import mmf
 
 pytestmark = pytest.mark.gpu
@@ -58,3 +61,35 @@ def test_8bit_moments_follow_the_32bit_ones(path):
         assert abs((got / want.double()).mean().item() - 1) <= 6 * (var / n) ** 0.5 + 1e-3
     moved = (p[8].double() / p[32].double()).mean().item()
     assert moved >= 1 - 6 * 2.3 / n ** 0.5
+
+
+def plain_codes(g, seed, tensor):
+    """The codes of m and v after a first step with beta 0.9 and 0.95 (0.1 g and 0.05 g^2 in fp32), by the draws of
+    the stream whose key takes the seed's lower half as the input streams do and its upper half mixed."""
+    key = I.mix_int(((seed & 0xFFFFFFFF) << 32) + tensor + I.mix_int(seed >> 32))
+    z = I._mix(torch.arange(1, (g.size + 1) // 2 + 1) * I._s64(I._GOLDEN) + I._s64(key)).numpy().view(np.uint64)
+    bits = np.stack([z & np.uint64(0xFFFFFFFF), z >> np.uint64(32)], 1).reshape(-1)[:g.size].astype(np.int64)
+    m, v = g * np.float32(1 - 0.9), (g * g) * np.float32(1 - 0.95)
+    return P.quantise(m, bits & 0xFFFF, 7, 3, 7, False)[0], P.quantise(v, bits >> 16, 14, 2, 15, True)[0]
+
+
+@pytest.mark.parametrize("path", ["arguments", "scalars"])
+def test_all_bits_of_the_seed_count(path):
+    """Seeds that differ in their upper half alone give other codes, those of their own streams."""
+    g = np.random.default_rng(2).standard_normal(2049).astype(np.float32)
+    gd = torch.from_numpy(g).to(DEV)
+    seen = []
+    for seed in (5, 5 + (1 << 32), 5 + (1 << 33), 5 + (1 << 63), (1 << 64) - 1):
+        ps = [torch.zeros(g.size, device=DEV) for _ in range(2)]
+        ts = [mmf.AdamWTensor(p, gd, **mmf.adamw_state(p, 8)) for p in ps]
+        if path == "scalars":
+            mmf.adamw_step(ts, step=1, lr=1e-3, scalars=mmf.adamw_scalars(step=1, lr=1e-3, seed=seed).to(DEV))
+        else:
+            mmf.adamw_step(ts, step=1, lr=1e-3, seed=seed)
+        for i, t in enumerate(ts):
+            m, v = plain_codes(g, seed, i)
+            assert np.array_equal(t.m.view(torch.uint8).cpu().numpy(), m)
+            assert np.array_equal(t.v.view(torch.uint8).cpu().numpy(), v)
+            seen.append(m)
+    # two independent draws round a value apart a third of the time in the mean
+    assert all((a != b).mean() > 0.1 for i, a in enumerate(seen) for b in seen[:i])
