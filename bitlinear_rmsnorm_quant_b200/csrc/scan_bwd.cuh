@@ -44,15 +44,31 @@ constexpr int kSbWarps = 4;    // warps per CTA, each on a segment of its own
 __device__ __forceinline__ f2 f2_bf16(uint32_t w) {
     return f2_make(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-// a bf16 pair raised to at least kScanClamp (-28 is a bf16 value); a NaN stays
+// a bf16 pair raised to at least kScanClamp (-28 is a bf16 value); a NaN stays, or (floor) becomes kScanClamp too
 __device__ __forceinline__ uint32_t clamp_bf16x2(uint32_t w) {
     uint32_t r;
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0xC1E0C1E0u));
     return r;
 }
+__device__ __forceinline__ uint32_t floor_bf16x2(uint32_t w) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0xC1E0C1E0u));
+    return r;
+}
 __device__ __forceinline__ f2 f2_exp_neg(f2 v) {  // e^-v
     const float2 a = f2_get(f2_mul(v, f2_set(-kLog2e)));
     return f2_make(ex2_ftz(a.x), ex2_ftz(a.y));
+}
+// e^-v of a v at least kScanClamp; of a NaN e^28
+__device__ __forceinline__ f2 f2_exp_neg_number(f2 v) {
+    const float2 a = f2_get(f2_mul(v, f2_set(-kLog2e)));
+    return f2_make(ex2_ftz(fminf(a.x, -kLog2e * kScanClamp)), ex2_ftz(fminf(a.y, -kLog2e * kScanClamp)));
+}
+// do g of a gate from ScanGates, a NaN where its pre-activation is one
+__device__ __forceinline__ f2 f2_gated(uint32_t wd, uint32_t wg, f2 g) {
+    uint32_t nan;
+    asm("set.nan.u32.bf16x2 %0, %1, %1;" : "=r"(nan) : "r"(wg));
+    return f2_mul(f2_bf16(wd | nan), g);
 }
 __device__ __forceinline__ uint32_t f2_to_bf16(f2 v) {
     const float2 a = f2_get(v);
@@ -61,14 +77,17 @@ __device__ __forceinline__ uint32_t f2_to_bf16(f2 v) {
 }
 
 // The gates of one token from its (clamped) pre-activations: one reciprocal
-// gives all three sigmoids (scan.cuh).
+// gives all three sigmoids (scan.cuh).  A NaN of f_pre makes the token's gates
+// NaN, which every output it has a part in is; one of c_pre or g_pre must not
+// reach the others (a NaN of f would spread over the whole sequence), so s and g
+// are numbers then: cp keeps the NaN of c_pre, and f2_gated puts back that of g_pre.
 struct ScanGates {
     f2 cp, ef, ec, eg, f, s, g;
     __device__ __forceinline__ ScanGates(uint32_t wf, uint32_t wc, uint32_t wg) {
         cp = f2_bf16(clamp_bf16x2(wc));
         ef = f2_exp_neg(f2_bf16(clamp_bf16x2(wf)));
-        ec = f2_exp_neg(cp);
-        eg = f2_exp_neg(f2_bf16(clamp_bf16x2(wg)));
+        ec = f2_exp_neg_number(cp);
+        eg = f2_exp_neg(f2_bf16(floor_bf16x2(wg)));
         const f2 one = f2_set(1.0f);
         const f2 df = f2_add(one, ef), dc = f2_add(one, ec), dg = f2_add(one, eg);
         const f2 dfc = f2_mul(df, dc);
@@ -141,7 +160,7 @@ __global__ void __launch_bounds__(kSbWarps * 32) mlgru_scan_bwd_maps_kernel(cons
             const ScanGates t(wf[i], wc[i], wg[i]);
             A = f2_mul(A, t.f);
             P = f2_fma(t.f, P, f2_mul(f2_mul(t.ef, t.f), f2_mul(t.cp, t.s)));
-            R = f2_fma(A, f2_mul(f2_bf16(wd[i]), t.g), R);
+            R = f2_fma(A, f2_gated(wd[i], wg[i], t.g), R);
         }
     }
     const float2 a = f2_get(A), q = f2_get(P), r = f2_get(R);
@@ -175,7 +194,7 @@ __device__ __forceinline__ void scan_back(const ScanBwdParams& p, int64_t at, in
         xc[i] = f2_mul(omf, f2_mul(t.s, f2_fma(t.cp, f2_mul(t.ec, t.s), f2_set(1.0f))));
         hs = f2_fma(t.f, hs, f2_mul(omf, c));
         fg[i] = t.f;
-        dg[i] = f2_mul(f2_bf16(wd[i]), t.g);
+        dg[i] = f2_gated(wd[i], wg[i], t.g);
         *reinterpret_cast<uint32_t*>(p.dg_pre + at + static_cast<int64_t>(i) * p.D) =
             f2_to_bf16(f2_mul(f2_mul(dg[i], hs), f2_mul(t.eg, t.g)));
     }
@@ -397,11 +416,11 @@ __global__ void __launch_bounds__(GW * 32) mlgru_scan_bwd_maps_tma_kernel(const 
             f2 f[kBatch], q[kBatch], x[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const ScanGates t(tile_pair<GW>(mine, 0, i0 + i), tile_pair<GW>(mine, 1, i0 + i),
-                                  tile_pair<GW>(mine, 2, i0 + i));
+                const uint32_t wg = tile_pair<GW>(mine, 2, i0 + i);
+                const ScanGates t(tile_pair<GW>(mine, 0, i0 + i), tile_pair<GW>(mine, 1, i0 + i), wg);
                 f[i] = t.f;
                 q[i] = f2_mul(f2_mul(t.ef, t.f), f2_mul(t.cp, t.s));
-                x[i] = f2_mul(f2_bf16(tile_pair<GW>(mine, 3, i0 + i)), t.g);
+                x[i] = f2_gated(tile_pair<GW>(mine, 3, i0 + i), wg, t.g);
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
@@ -476,14 +495,15 @@ __global__ void __launch_bounds__(GW * 32, 16 / GW) mlgru_scan_bwd_tma_kernel(co
         // of each token: what dh is multiplied with for df_pre, dc_pre and the token before, and do g
         f2 xf[kSbSub], xc[kSbSub], fg[kSbSub], dg[kSbSub];
         const auto ahead = [&](int i) {
-            const ScanGates t(tile_pair<GW>(mine, 0, i), tile_pair<GW>(mine, 1, i), tile_pair<GW>(mine, 2, i));
+            const uint32_t wg = tile_pair<GW>(mine, 2, i);
+            const ScanGates t(tile_pair<GW>(mine, 0, i), tile_pair<GW>(mine, 1, i), wg);
             const f2 omf = f2_mul(t.ef, t.f);   // 1 - f
             const f2 c = f2_mul(t.cp, t.s);
             xf[i] = f2_mul(f2_fma(c, f2_set(-1.0f), hs), f2_mul(t.f, omf));
             xc[i] = f2_mul(omf, f2_mul(t.s, f2_fma(t.cp, f2_mul(t.ec, t.s), f2_set(1.0f))));
             hs = f2_fma(t.f, hs, f2_mul(omf, c));
             fg[i] = t.f;
-            dg[i] = f2_mul(f2_bf16(tile_pair<GW>(mine, 3, i)), t.g);
+            dg[i] = f2_gated(tile_pair<GW>(mine, 3, i), wg, t.g);
             *reinterpret_cast<uint32_t*>(mine + 2 * sb_tile(GW) + i * (128 * GW)) =
                 f2_to_bf16(f2_mul(f2_mul(dg[i], hs), f2_mul(t.eg, t.g)));
         };
