@@ -21,7 +21,7 @@
 //
 // Bound and measured: 28 bytes an element with fp32 moments and gradients, 14
 // with 8-bit moments and bf16 gradients.  One 1.3B layer set (51.4 M elements,
-// fp32): 212 us, 6.7 TB/s, the copy rate.  Two 2.7B layer sets (158.6 M, 8
+// fp32): 213 us, 6.7 TB/s, the copy rate.  Two 2.7B layer sets (158.6 M, 8
 // bits, bf16 gradients and copy, 16 bytes): 430 us in a short run, 5.9 TB/s,
 // 487 us where calls follow one another for long; there the noise and the
 // packing of the codes bind, 71 instructions an element, the ALU pipe 71% busy.

@@ -5,11 +5,12 @@
 // An id outside [0, V) (a padded place) gives a row of zeros and no gradient.
 //
 // Bound by HBM and, for small batches, by launches.  Measured: lookup of 131072
-// rows of 2048 from a bf16 table of 50257, 109 us (5.9 TB/s counting each row
-// of the table once); gradient of 8192 tokens for a table of 32000 x 2560, 76
-// us, 60 of them the sums and zeros at 5.5 TB/s behind the sort's 14; of 131072
-// tokens for 50257 x 2048, 187 us, 144 of them at 5.9 TB/s, 30 the sort's and
-// 13 the join's; 511 tokens added to a table, 4 us (9 us a call on the host).
+// rows of 2048 from a bf16 table of 50257, 109 us on the device (5.9 TB/s
+// counting each row of the table once), 117 where calls follow one another;
+// gradient of 8192 tokens for a table of 32000 x 2560, 75 us, 60 of them the sums
+// and zeros at 5.5 TB/s behind the sort's 14; of 131072 tokens for 50257 x 2048,
+// 190 us, 144 of them at 5.9 TB/s, 30 the sort's and 14 the join's; 511 tokens
+// added to a table, 5 us (9 us a call on the host).
 #pragma once
 #include "common.cuh"
 
@@ -30,7 +31,7 @@ __device__ __forceinline__ int64_t embed_id(const Id* __restrict__ ids, int64_t 
 // the CTAs alike.  x is written past L2 so that the frequent words' rows stay
 // there.  Index is what numbers the groups: 32 bits where they fit.  A thread
 // divides once and steps from group to group by kEmbedThreads' quotient and
-// remainder (131072 x 2048: 109 us; with a division for each, 116 us at three
+// remainder (131072 x 2048: 109 us on the device; with a division for each, 116 us at three
 // instructions a cycle).
 constexpr int kFwdItems = 4;
 

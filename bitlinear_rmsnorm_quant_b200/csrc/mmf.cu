@@ -735,9 +735,10 @@ mmf_status check_scan_shape(int64_t B, int64_t T, int64_t D) {
 // whole kSbSub-token steps.  Segments are as many as keep the time of all waves
 // of resident CTAs shortest, a CTA's time being its steps, about two steps to
 // begin and end, and 0.1 steps for each other segment whose map it folds: four
-// waves at most, and less than one where few channels would make segments of so
-// few steps that the fold takes longer than they (2048 tokens of 512 channels:
-// 14.4 us, 26.5 with a whole wave; 131072 of 64 channels: 78 and 185).
+// waves at most (16 warps an SM; the CTAs of three warps are 15, and without
+// tensor copies it is 12), and less than one where few channels would make
+// segments of so few steps that the fold takes longer than they (2048 tokens of
+// 512 channels: 14.4 us, 26.5 with a whole wave; 131072 of 64 channels: 78 and 185).
 struct ScanBwdPlan {
     bool one_launch, tma;
     int gw, groups, subs, subs_per_seg, segments;

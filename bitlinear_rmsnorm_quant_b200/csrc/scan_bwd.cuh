@@ -26,10 +26,11 @@
 // Bound and measured: 14 bytes a token and channel (f, c, g, do read, the
 // gradients written) are the least; the second launch reads the first four
 // again, from L2 where they fit, and the kept maps are a byte written and read,
-// 24 in all.  16 x 2048 x 2048: 264 us, 1.55 GB at 5.9 TB/s.  4 x 2048 x 2048:
-// 67 us, 31 for the maps (4.8 TB/s) and 37 for the gradients, which a quarter
-// of the reads find in L2 and 72 instructions a channel pair at two a cycle
-// bind (16 warps of 121 registers an SM; 24 of 80, with half the tokens at a
+// 24 in all.  16 x 2048 x 2048: 262 us on the device, 1.55 GB at 5.9 TB/s (276
+// where calls follow one another).  4 x 2048 x 2048: 68 us, 29 for the maps (4.8
+// TB/s) and 39 for the gradients, which a quarter of the reads find in L2 and 76
+// instructions a channel pair at two a cycle bind (73 where calls follow one
+// another; 16 warps of 122 registers an SM; 24 of 80, with half the tokens at a
 // time, took 72 us).
 #pragma once
 #include "common.cuh"

@@ -269,11 +269,12 @@ int mmf_embed_bwd(const void* ids, const uint16_t* dx, float scale, int64_t V,
  *   dc_pre = bf16_rn(dh_t (1 - f) s (1 + c_pre (1 - s)))
  *   dg_pre = bf16_rn(do h_t g (1 - g))
  * in fp32, sigma by the hardware exponential and reciprocal as there.
- * Pre-activations below -28 (-infinity too) count as -28, as there: gates and
- * 1 - gates of less than 7e-13 are off by up to that much, and the outputs they
- * scale by up to 1e-11 of the state's and the gradient's size, relative to
- * themselves without bound.  A NaN reaches the outputs that these formulas make
- * NaN and no others.  f_pre, c_pre, g_pre, d_o (the gradient of o) and the outputs
+ * Pre-activations below -28 (-infinity too) count as -28, as there: gates of
+ * less than 7e-13 are off by up to that much, and the outputs they scale by up
+ * to 2e-11 of the state's and the gradient's size, relative to themselves without
+ * bound.  A NaN reaches the outputs that these formulas make NaN and no others;
+ * an infinite input's outputs may be NaN where the formulas make them infinite.
+ * f_pre, c_pre, g_pre, d_o (the gradient of o) and the outputs
  * df_pre, dc_pre, dg_pre: bf16 [B][T][D]; h0, dh_last (may be NULL) and dh0
  * (may be NULL: not wanted): fp32 [B][D].  Sizes as mmf_mlgru_scan.  The
  * outputs and the workspace must not overlap the inputs or one another.  T = 0 copies dh_last
