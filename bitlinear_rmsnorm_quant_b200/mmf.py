@@ -533,6 +533,7 @@ def adamw_step(tensors, step: int, lr: float, beta1: float = 0.9, beta2: float =
                grad_scale: float = 1.0, seed: int | None = None, scalars: torch.Tensor | None = None, stream=None) -> None:
     """One AdamW step over a sequence of AdamWTensor, in place; `step` counts from 1.  With `scalars` (uint8[32]
     on the device, see adamw_scalars) the kernel takes lr, the bias corrections, grad_scale and seed from there.
+    A graph captured without them repeats its step's on every replay, the noise too.
     `seed` is that of the rounding noise of 8-bit moments (without any it changes nothing): the step when not given;
     a caller that gives one gives another at every step, or the moments are biased."""
     tensors = list(tensors)
